@@ -1,4 +1,4 @@
-"""ctypes binding of libuno.so (include/uno.h). Argument marshalling only.
+"""ctypes binding of libuno.so (include/uno.h, include/uno_layers.h). Argument marshalling only.
 
 Each function has the C entry point's name and takes torch tensors (device memory) where
 the C ABI takes device pointers; it checks shapes/dtypes enough to build the call, passes
@@ -26,6 +26,11 @@ EXPORTED = (
     "uno_block_verify_workspace_size", "uno_block_verify_min_workspace_size", "uno_block_verify",
     "uno_block_verify_noalloc",
     "uno_tv_loss_workspace_size", "uno_tv_loss", "uno_block_noise",
+)
+# include/uno_layers.h
+EXPORTED_LAYERS = (
+    "uno_rms_norm_fp8", "uno_fp8_quantize", "uno_fp8_gated_lora_linear_workspace_size", "uno_fp8_gated_lora_linear",
+    "uno_token_logprobs", "uno_token_logprobs_grad",
 )
 
 
@@ -75,6 +80,16 @@ def load(path: str | os.PathLike | None = None) -> ctypes.CDLL:
     for fn in ("uno_gated_lora_linear", "uno_block_verify", "uno_tv_loss"):
         getattr(lib, fn).restype = ctypes.c_int
     lib.uno_read_device_status.restype = ctypes.c_int
+    lib.uno_rms_norm_fp8.argtypes = [_vp, _vp, _vp, ctypes.c_int, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp]
+    lib.uno_fp8_quantize.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i32, _vp, _vp, _vp]
+    lib.uno_fp8_gated_lora_linear_workspace_size.restype = _sz
+    lib.uno_fp8_gated_lora_linear_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+    lib.uno_fp8_gated_lora_linear.argtypes = [_vp] * 8 + [_f32, _i64, _i64, _i64, _i64, _vp, ctypes.c_int, _vp, _sz, _vp]
+    lib.uno_token_logprobs.argtypes = [_vp, ctypes.c_int, _i64, _i64, _f32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.uno_token_logprobs_grad.argtypes = [_vp, ctypes.c_int, _i64, _i64, _f32] + [_vp] * 7
+    for fn in ("uno_rms_norm_fp8", "uno_fp8_quantize", "uno_fp8_gated_lora_linear", "uno_token_logprobs",
+               "uno_token_logprobs_grad"):
+        getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -207,3 +222,128 @@ def uno_block_noise(clean_tokens, uniforms, V, noised_tokens, row_gate=None, str
     _check(load().uno_block_noise(_ptr(clean_tokens), _ptr(uniforms), B, K, int(V), _ptr(noised_tokens),
                                   _ptr(row_gate), _stream(stream)))
     return noised_tokens
+
+
+# ---------------------------------------------------------------------------------------
+# include/uno_layers.h: every tensor's shape, dtype and device is checked here, and the call
+# runs on the tensors' device whichever one is current.
+_F8 = torch.float8_e4m3fn
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _arg(name, t, shape, dtype, device):
+    """Device address of tensor `t` (None passes NULL) after checking what it has to be."""
+    if t is None:
+        return None
+    p = _ptr(t)
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return p
+
+
+def _matrix(name, t, dtypes):
+    _ptr(t)
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return t.shape
+
+
+def _call(fn, device, stream, *args):
+    """One library call on `device`, enqueued on `stream` (default: the device's current one)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream))
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def uno_rms_norm_fp8(x, weight, eps, out_q=None, out_scale=None, residual=None, out_residual=None, out_y=None,
+                     stream=None):
+    """RMS norm of x (+ residual) with e4m3 values and a scale per 128 columns, and / or the
+    norm in x's dtype (see include/uno_layers.h)."""
+    M, d = _matrix("x", x, _FLOATS)
+    dev, t = x.device, x.dtype
+    _call(load().uno_rms_norm_fp8, dev, stream, _ptr(x), _arg("residual", residual, (M, d), t, dev),
+          _arg("weight", weight, (d,), t, dev), _dtype_code(x), M, d, float(eps),
+          _arg("out_residual", out_residual, (M, d), t, dev), _arg("out_q", out_q, (M, d), _F8, dev),
+          _arg("out_scale", out_scale, (M, _blocks(d)), torch.float32, dev), _arg("out_y", out_y, (M, d), t, dev))
+
+
+def uno_fp8_quantize(x, out_q, out_scale, block_rows=1, stream=None):
+    """e4m3 values and scales of x by block_rows x 128 blocks, block_rows 1 (activations) or
+    128 (weights) (see include/uno_layers.h)."""
+    M, d = _matrix("x", x, _FLOATS)
+    dev, rows = x.device, int(block_rows)
+    _call(load().uno_fp8_quantize, dev, stream, _ptr(x), _dtype_code(x), M, d, rows,
+          _arg("out_q", out_q, (M, d), _F8, dev),
+          _arg("out_scale", out_scale, (M if rows == 1 else _blocks(M), _blocks(d)), torch.float32, dev))
+
+
+def uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank) -> int:
+    return int(load().uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank))
+
+
+def uno_fp8_gated_lora_linear(x_q, x_scale, w_q, w_scale, y, x=None, lora_a=None, lora_b=None, row_gate=None,
+                              scale=1.0, workspace=None, stream=None):
+    """y = (x_q x_scale)(w_q w_scale)^T + scale * diag(row_gate) (x lora_a^T) lora_b^T, the
+    adapter only where lora_a is given (see include/uno_layers.h)."""
+    M, d_in = _matrix("x_q", x_q, (_F8,))
+    d_out = _matrix("w_q", w_q, (_F8,))[0]
+    dev, bf, f32 = x_q.device, torch.bfloat16, torch.float32
+    rank = 0 if lora_a is None else _matrix("lora_a", lora_a, (bf,))[0]
+    _matrix("y", y, _FLOATS)
+    ws, nb = None, 0
+    if rank:
+        nb = uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank)
+        made = workspace is None
+        ws, nb = _workspace(nb, dev, workspace)
+        if ws is not None and ws.device != dev:
+            raise ValueError(f"workspace is on {ws.device}, the tensors are on {dev}")
+        if made and ws is not None and stream is not None:
+            ws.record_stream(stream)  # it may not be handed out again before this stream is done with it
+    _call(load().uno_fp8_gated_lora_linear, dev, stream, _ptr(x_q),
+          _arg("x_scale", x_scale, (M, _blocks(d_in)), f32, dev), _arg("w_q", w_q, (d_out, d_in), _F8, dev),
+          _arg("w_scale", w_scale, (_blocks(d_out), _blocks(d_in)), f32, dev), _arg("x", x, (M, d_in), bf, dev),
+          _arg("lora_a", lora_a, (rank, d_in), bf, dev), _arg("lora_b", lora_b, (d_out, rank), bf, dev),
+          _arg("row_gate", row_gate, (M,), f32, dev), float(scale), M, d_in, d_out, rank,
+          _arg("y", y, (M, d_out), y.dtype, dev), _dtype_code(y), _ptr(ws), nb)
+    return y
+
+
+def uno_token_logprobs(logits, tokens, out_logprob=None, temperature=1.0, out_entropy=None, out_stats=None,
+                       out_top_ids=None, out_top_logprobs=None, stream=None):
+    """Log probability of each row's token, entropy, the most probable tokens (as many as
+    out_top_ids has columns), and the statistics the gradient needs; rows whose token is not
+    in [0, V) are left out (see include/uno_layers.h)."""
+    N, V = _matrix("logits", logits, _FLOATS)
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    top = 0 if out_top_ids is None else _matrix("out_top_ids", out_top_ids, (i32,))[1]
+    _call(load().uno_token_logprobs, dev, stream, _ptr(logits), _dtype_code(logits), N, V, float(temperature),
+          _arg("tokens", tokens, (N,), i32, dev), top, _arg("out_logprob", out_logprob, (N,), f32, dev),
+          _arg("out_entropy", out_entropy, (N,), f32, dev), _arg("out_stats", out_stats, (N, 2), f32, dev),
+          _arg("out_top_ids", out_top_ids, (N, top), i32, dev) if top else None,
+          _arg("out_top_logprobs", out_top_logprobs, (N, top), f32, dev) if top else None)
+
+
+def uno_token_logprobs_grad(logits, tokens, stats, grad_logits, grad_logprob=None, entropy=None, grad_entropy=None,
+                            temperature=1.0, stream=None):
+    """Gradient of uno_token_logprobs' log probabilities and entropies with respect to the
+    logits; grad_logits may be logits itself (see include/uno_layers.h)."""
+    N, V = _matrix("logits", logits, _FLOATS)
+    dev, f32 = logits.device, torch.float32
+    _call(load().uno_token_logprobs_grad, dev, stream, _ptr(logits), _dtype_code(logits), N, V, float(temperature),
+          _arg("tokens", tokens, (N,), torch.int32, dev), _arg("stats", stats, (N, 2), f32, dev),
+          _arg("entropy", entropy, (N,), f32, dev), _arg("grad_logprob", grad_logprob, (N,), f32, dev),
+          _arg("grad_entropy", grad_entropy, (N,), f32, dev),
+          _arg("grad_logits", grad_logits, (N, V), logits.dtype, dev))

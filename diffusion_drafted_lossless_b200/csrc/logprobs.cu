@@ -1,0 +1,593 @@
+// logprobs.cu — log probabilities of given tokens, entropy, the most probable alternatives,
+// and the gradient.
+//
+//   z = (x - ref) / T,  s = sum exp(z),  a = sum exp(z) z   (ref: near the row's maximum)
+//   log p_v = (x_v - max) / T - log s_max,   entropy = log s_max - a_max / s_max
+// where s_max, a_max are the sums moved to ref = max. exp is ex2 of (x - ref) (log2 e / T);
+// x - ref is taken before the product, so values of any size keep their differences.
+//
+// One pass over the row (bound: HBM). A row goes to a cluster of S CTAs, each with a run of
+// it; a thread streams 16-byte pieces, kUnroll of them in flight. The first pieces of all
+// threads are a sample: its maximum is every thread's first reference, so that references
+// move (and sums are rescaled) only where a value lies 64 octaves above; and the top_n-th
+// largest of the sample's 64 group maxima is a value that at least top_n tokens reach, so
+// only elements at or above it (a few hundred of a row) are candidates for the alternatives.
+// They are appended to a list in shared memory, and ranked at the end by counting, for each,
+// the candidates above it, value first and id second. A list that overflows (a row in
+// ascending order, a row of equal values) is no loss: its entries are real tokens, so the
+// top_n-th best of them bounds the search and the run is read again for what beats it, until
+// the list holds everything.
+#include <cmath>
+#include <type_traits>
+
+#include "layers.cuh"
+
+namespace uno {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kUnroll = 4;
+constexpr int kGroups = 64;     // groups of 8 lanes whose maxima bound the search
+constexpr int kList = 2048;     // candidates held; the second half keeps the latest ones
+constexpr int kMaxTop = 32;
+constexpr int kMaxSplit = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// an exponent no lower than that of nothing; a NaN stays one
+__device__ __forceinline__ float exponent(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-2000.f));
+    return y;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[kVec<T>]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(w[i]);
+            f[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+}
+
+// One value. (Not __ldg of a __nv_bfloat16: that is an asm statement without volatile, which
+// the compiler may run ahead of the condition that keeps its address inside the row.)
+template <typename T>
+__device__ __forceinline__ float load_one(const T* p) {
+    if constexpr (std::is_same_v<T, float>) return __ldg(p);
+    else return bf16_lo(__ldg(reinterpret_cast<const unsigned short*>(p)));
+}
+
+// the largest of a piece (NaN passed over)
+template <typename T>
+__device__ __forceinline__ float piece_max(const uint4& v) {
+    if constexpr (std::is_same_v<T, float>) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+        auto h = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(v.x), h(v.y)), __hmax2(h(v.z), h(v.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+}
+
+// A thread's running sums over what it has read: relative to ref, in octaves (z = arg ln 2)
+struct Sums {
+    float ref, max, s, a;
+};
+
+// the sums moved to another reference (delta = (old - new) c, at most 0 or with s = 0)
+__device__ __forceinline__ void move_ref(Sums& t, float to, float c) {
+    if (t.s > 0.f) {
+        const float d = (t.ref - to) * c, f = ex2(d);
+        t.a = f * fmaf(d, t.s, t.a);
+        t.s *= f;
+        if (f == 0.f) t.a = 0.f;
+    }
+    t.ref = to;
+}
+
+__device__ __forceinline__ void add_one(Sums& t, float x, float c) {
+    const float arg = exponent((x - t.ref) * c);  // (ref is finite or +inf: -inf has no weight)
+    const float e = ex2(arg);
+    t.s += e;
+    t.a = fmaf(e, arg, t.a);
+}
+
+// candidates found so far by this CTA, and the bound that new ones have to reach
+struct Search {
+    unsigned long long* list;
+    unsigned int* count;
+};
+
+__device__ __forceinline__ void append(const Search& q, float x, uint32_t id) {
+    const unsigned int at = atomicAdd(q.count, 1u);
+    const unsigned int slot = at < kList ? at : kList / 2 + at % (kList / 2);
+    q.list[slot] = pack_candidate(float_key(x), id);
+}
+
+struct Args {
+    int64_t V;
+    float c, inv_t;            // log2 e / T, 1 / T
+    const int32_t* tokens;
+    int top_n;
+    float *logprob, *entropy, *stats;
+    int32_t* top_ids;
+    float* top_lp;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_peer_f32(const float* p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long ld_peer_u64(const unsigned long long* p, uint32_t rank) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* __restrict__ logits, const Args p) {
+    constexpr int VE = kVec<T>;
+    __shared__ unsigned long long list[kList];
+    __shared__ unsigned long long best[kMaxTop];          // this run's top candidates, in order
+    __shared__ unsigned long long merged[kMaxSplit * kMaxTop];
+    __shared__ float group[kGroups];
+    __shared__ float part[kWarps][4];
+    __shared__ float run[4];                               // this run's ref, max, s, a
+    __shared__ float s_ref, s_bound;
+    __shared__ unsigned int s_count;
+    __shared__ unsigned long long s_kth;
+
+    const uint32_t S = cluster_size(), rank = cluster_rank();
+    const int64_t n = blockIdx.x / S;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int k = p.top_n;
+
+    const int32_t tok = p.tokens ? p.tokens[n] : 0;
+    if (tok < 0 || tok >= p.V) {  // a row that is left out (the whole cluster leaves)
+        if (rank == 0) {
+            if (tid == 0) {
+                if (p.logprob) p.logprob[n] = 0.f;
+                if (p.entropy) p.entropy[n] = 0.f;
+                if (p.stats) p.stats[2 * n] = p.stats[2 * n + 1] = 0.f;
+            }
+            if (tid < k) {
+                p.top_ids[n * k + tid] = -1;
+                p.top_lp[n * k + tid] = -INFINITY;
+            }
+        }
+        return;
+    }
+
+    const T* row = logits + n * p.V;
+    // 16-byte pieces from the first aligned element on; the elements before and behind them
+    // are taken one by one by the first CTA
+    const int64_t mis = (int64_t)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    const int64_t head = mis ? (VE - mis < p.V ? VE - mis : p.V) : 0;
+    const int64_t pieces = (p.V - head) / VE, tail = p.V - head - pieces * VE;
+    const int64_t lo = pieces * rank / S, hi = pieces * (rank + 1) / S;
+    const uint4* body = reinterpret_cast<const uint4*>(row + head);
+    // edge element tid of the first CTA: id, or -1
+    int64_t edge = -1;
+    if (rank == 0 && tid < head) edge = tid;
+    if (rank == 0 && tid >= 32 && tid - 32 < tail) edge = p.V - tail + (tid - 32);
+    const float edge_x = load_one(row + (edge >= 0 ? edge : 0));
+
+    const Search q{list, &s_count};
+    const float ninf = -INFINITY;
+    uint4 v[kUnroll];
+    const uint32_t none = std::is_same_v<T, float> ? 0xFF800000u : 0xFF80FF80u;  // -inf
+    auto load = [&](int64_t i0) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t i = i0 + (int64_t)u * kThreads;
+            v[u] = i < hi ? ld_stream_v4(body + i) : make_uint4(none, none, none, none);
+        }
+    };
+
+    // ---- the sample: every thread's first pieces ----
+    load(lo + tid);
+    float m = ninf;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) m = fmaxf(m, piece_max<T>(v[u]));
+    float g = m;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(kFullMask, g, o));
+    if ((lane & 7) == 0) group[tid >> 3] = g;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    if (warp == 0) {
+        const float g0 = group[lane], g1 = group[lane + 32];
+        if (lane == 0) s_bound = ninf;
+        const float top = warp_max(fmaxf(g0, g1));
+        if (k > 0) {
+            // ranks among the group maxima (equal ones by position): the k-th bounds the search
+            int r0 = 0, r1 = 0;
+            for (int j = 0; j < kGroups; ++j) {
+                const float o = group[j];
+                r0 += o > g0 || (o == g0 && j < lane);
+                r1 += o > g1 || (o == g1 && j < lane + 32);
+            }
+            __syncwarp();
+            if (r0 == k - 1) s_bound = g0;
+            if (r1 == k - 1) s_bound = g1;
+        }
+        if (lane == 0) s_ref = fmaxf(top, -3.402823466e38f);  // finite where the sample is all -inf
+    }
+    __syncthreads();
+
+    Sums t{s_ref, ninf, 0.f, 0.f};
+    const float c = p.c;
+    const float bound = s_bound;
+    // (the id of body element 0; ids are below 2^31)
+    const uint32_t id0 = (uint32_t)head;
+
+    auto candidates = [&](const uint4& w, int64_t i) {
+        float f[VE];
+        unpack<T>(w, f);
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+            if (f[e] >= bound && f[e] > ninf) append(q, f[e], id0 + (uint32_t)(i * VE + e));
+    };
+
+    if (edge >= 0) {
+        const float x = edge_x;
+        if (!((x - t.ref) * c <= 64.f)) move_ref(t, fmaxf(x, t.ref), c);
+        t.max = fmaxf(t.max, x);
+        add_one(t, x, c);
+        if (k > 0 && x >= bound && x > ninf) append(q, x, (uint32_t)edge);
+    }
+    for (int64_t i0 = lo + tid; i0 < hi;) {
+        float pm[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) pm[u] = piece_max<T>(v[u]);
+        float cm = ninf;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) cm = fmaxf(cm, pm[u]);
+        t.max = fmaxf(t.max, cm);
+        if ((cm - t.ref) * c > 64.f) move_ref(t, cm, c);
+        if (k > 0 && cm >= bound) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (pm[u] >= bound) candidates(v[u], i0 + (int64_t)u * kThreads);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float f[VE];
+            unpack<T>(v[u], f);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) add_one(t, f[e], c);
+        }
+        i0 += (int64_t)kUnroll * kThreads;
+        if (i0 < hi) load(i0);
+    }
+
+    // ---- this run's sums, relative to its maximum ----
+    auto combine = [&](float mx) {  // the block's sums at reference mx, valid in warp 0
+        if (t.s == 0.f) t.a = 0.f;
+        move_ref(t, mx, c);
+        const float s = warp_sum(t.s), a = warp_sum(t.a);
+        if (lane == 0) part[warp][1] = s, part[warp][2] = a;
+    };
+    const float wm = warp_max(t.max);
+    if (lane == 0) part[warp][0] = wm;
+    __syncthreads();
+    const float mx = warp_max(part[lane & (kWarps - 1)][0]);
+    combine(mx);
+    __syncthreads();
+    if (warp == 0) {
+        const float s = warp_sum(lane < kWarps ? part[lane][1] : 0.f);
+        const float a = warp_sum(lane < kWarps ? part[lane][2] : 0.f);
+        if (lane == 0) run[0] = run[1] = mx, run[2] = s, run[3] = a;
+    }
+
+    // ---- this run's best k ----
+    if (k > 0) {
+        unsigned long long kth = 0;  // candidates have to beat it (0: all do)
+        for (;;) {
+            const unsigned int found = s_count;
+            const unsigned int held = found < kList ? found : kList;
+            // rank of each held candidate (all differ: ids do)
+            for (unsigned int j = tid; j < held; j += kThreads) {
+                const unsigned long long mine = list[j];
+                int r = 0;
+                for (unsigned int o = 0; o < held && r < k; ++o) r += list[o] > mine;
+                if (r < k) best[r] = mine;
+                if (r == k - 1) s_kth = mine;
+            }
+            if (found <= kList) {
+                if (tid >= (int)held && tid < k) best[tid] = 0;
+                __syncthreads();
+                break;
+            }
+            // more were found than are held: read the run again for what beats the k-th held
+            __syncthreads();
+            kth = s_kth;
+            if (tid == 0) s_count = 0;
+            __syncthreads();
+            auto again = [&](float x, uint32_t id) {
+                if (x > ninf && pack_candidate(float_key(x), id) >= kth) append(q, x, id);
+            };
+            if (edge >= 0) again(edge_x, (uint32_t)edge);
+            for (int64_t i = lo + tid; i < hi; i += kThreads) {
+                const uint4 w = __ldg(body + i);
+                float f[VE];
+                unpack<T>(w, f);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) again(f[e], id0 + (uint32_t)(i * VE + e));
+            }
+            __syncthreads();
+        }
+    } else {
+        __syncthreads();
+    }
+
+    // ---- the runs of a cluster, joined by its first CTA ----
+    __syncwarp();
+    if (S > 1) {
+        cluster_sync();
+        if (rank == 0) {
+            if (tid < (int)S * k) merged[tid] = ld_peer_u64(&best[tid % k], tid / k);
+            if (warp == kWarps - 1) {
+                const bool in = lane < (int)S;
+                Sums r{ninf, ninf, 0.f, 0.f};
+                if (in) {
+                    r.ref = ld_peer_f32(&run[0], lane);
+                    r.max = r.ref;
+                    r.s = ld_peer_f32(&run[2], lane);
+                    r.a = ld_peer_f32(&run[3], lane);
+                }
+                const float all = warp_max(r.max);
+                move_ref(r, all, c);
+                const float s = warp_sum(r.s), a = warp_sum(r.a);
+                __syncwarp();
+                if (lane == 0) part[0][0] = all, part[0][1] = s, part[0][2] = a;
+            }
+        }
+        __syncthreads();
+        __syncwarp();
+        cluster_sync();
+        if (rank != 0) return;
+        if (tid < k) best[tid] = 0;
+        __syncthreads();
+        if (tid < (int)S * k && merged[tid]) {
+            int r = 0;
+            for (int o = 0; o < (int)S * k; ++o) r += merged[o] > merged[tid];
+            if (r < k) best[r] = merged[tid];
+        }
+    } else if (tid == 0) {
+        part[0][0] = run[1], part[0][1] = run[2], part[0][2] = run[3];
+    }
+    __syncthreads();
+    const float top = part[0][0], s = part[0][1], a = part[0][2];
+    const bool empty = top == ninf && s == 0.f;  // nothing can be produced
+    const float logs = empty ? 0.f : logf(s);
+    if (tid == 0) {
+        if (p.logprob) {
+            const float x = load_one(row + tok);
+            p.logprob[n] = empty ? ninf : (x - top) * p.inv_t - logs;
+        }
+        if (p.entropy) p.entropy[n] = empty ? 0.f : fmaf(-kLn2, a / s, logs);
+        if (p.stats) {
+            p.stats[2 * n] = top;
+            p.stats[2 * n + 1] = logs;
+        }
+    }
+    if (tid < k) {
+        const unsigned long long b = best[tid];
+        p.top_ids[n * k + tid] = b ? (int32_t)candidate_id(b) : -1;
+        p.top_lp[n * k + tid] = b ? (key_float(candidate_key(b)) - top) * p.inv_t - logs : ninf;
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// gradient: elementwise from the row's statistics. A CTA takes kGradPieces x 256 pieces of a
+// row, so the row's facts are read once for them.
+// ---------------------------------------------------------------------------------------
+constexpr int kGradThreads = 256, kGradPieces = 4;
+
+struct GradArgs {
+    int64_t V;
+    float c, inv_t;
+    const int32_t* tokens;
+    const float *stats, *entropy, *g_lp, *g_ent;
+    int chunks;  // CTAs per row
+};
+
+// (logits may be grad itself: no restrict and no read-only loads. A thread reads its pieces
+// before it writes them.)
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const T* logits, T* grad, const GradArgs p) {
+    constexpr int VE = kVec<T>;
+    const int64_t n = blockIdx.x / p.chunks;
+    const int chunk = (int)(blockIdx.x - n * p.chunks), tid = threadIdx.x;
+    const T* row = logits + n * p.V;
+    T* out = grad + n * p.V;
+    const int32_t tok = p.tokens ? p.tokens[n] : 0;
+    const float max = p.stats[2 * n], logs = p.stats[2 * n + 1];
+    const bool zero = tok < 0 || tok >= p.V || max == -INFINITY;
+    const float gl = !zero && p.g_lp ? p.g_lp[n] * p.inv_t : 0.f;
+    const float ge = !zero && p.g_ent ? p.g_ent[n] * p.inv_t : 0.f;
+    const float h = !zero && p.g_ent ? p.entropy[n] : 0.f;
+    // d = -p (gl + ge (log p + h)) = p (base + slope arg), arg = log2 p
+    const float l2 = logs * kLog2e, base = -fmaf(ge, h, gl), slope = -ge * kLn2;
+    auto one = [&](float x, int64_t id) {
+        const float arg = exponent(fmaf(x - max, p.c, -l2));
+        float d = ex2(arg) * fmaf(slope, arg, base);
+        if (id == tok) d += gl;
+        return zero ? 0.f : d;
+    };
+    auto put = [&](int64_t id, float d) {
+        if constexpr (std::is_same_v<T, float>) out[id] = d;
+        else out[id] = __float2bfloat16_rn(d);
+    };
+    auto get = [&](int64_t id) -> float {
+        if constexpr (std::is_same_v<T, float>) return row[id];
+        else return __bfloat162float(row[id]);
+    };
+    const int64_t mis = (int64_t)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    const int64_t head = mis ? (VE - mis < p.V ? VE - mis : p.V) : 0;
+    // (rows of grad are as aligned as those of logits: both tensors start on 16 bytes)
+    const int64_t pieces = (p.V - head) / VE, tail = p.V - head - pieces * VE;
+    if (chunk == 0) {
+        int64_t id = -1;
+        if (tid < head) id = tid;
+        if (tid >= 32 && tid - 32 < tail) id = p.V - tail + (tid - 32);
+        if (id >= 0) put(id, one(get(id), id));
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(row + head);
+    uint4* dst = reinterpret_cast<uint4*>(out + head);
+    const int64_t i0 = (int64_t)chunk * (kGradThreads * kGradPieces) + tid;
+    uint4 v[kGradPieces];
+#pragma unroll
+    for (int u = 0; u < kGradPieces; ++u) {
+        const int64_t i = i0 + u * kGradThreads;
+        v[u] = i < pieces && !zero ? src[i] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kGradPieces; ++u) {
+        const int64_t i = i0 + u * kGradThreads;
+        if (i >= pieces) continue;
+        float f[VE];
+        unpack<T>(v[u], f);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] = one(f[e], head + i * VE + e);
+        if constexpr (std::is_same_v<T, float>)
+            dst[i] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                __float_as_uint(f[3]));
+        else
+            dst[i] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                pack_bf16(f[6], f[7]));
+    }
+}
+
+template <typename T>
+uno_status logprobs_launch(const void* logits, int64_t N, const Args& p, cudaStream_t stream) {
+    const int sms = device_sms();
+    if (sms == 0) return set_error(UNO_ERR_CUDA, "the current device's properties cannot be read");
+    // CTAs per row: as many as fill the GPU twice, while each still has a few turns of work
+    int S = 1;
+    while (S < kMaxSplit && N * S * 2 <= 2 * (int64_t)sms && p.V >= (int64_t)S * 2 * kThreads * kVec<T>) S *= 2;
+    if (N * S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many rows");
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(N * S));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, static_cast<const T*>(logits), p),
+                      "launch(token logprobs)");
+}
+
+template <typename T>
+uno_status grad_launch(const void* logits, void* grad, int64_t N, GradArgs p, cudaStream_t stream) {
+    const int64_t pieces = p.V / kVec<T> + 1, per = kGradThreads * kGradPieces;
+    const int64_t chunks = (pieces + per - 1) / per;
+    if (chunks * N > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many logits for one launch");
+    p.chunks = (int)chunks;
+    logprobs_grad_kernel<T><<<(unsigned)(chunks * N), kGradThreads, 0, stream>>>(static_cast<const T*>(logits),
+                                                                                static_cast<T*>(grad), p);
+    return check_cuda(cudaGetLastError(), "launch(token logprobs gradient)");
+}
+
+uno_status check_rows(uno_dtype dtype, int64_t N, int64_t V, float temperature) {
+    if (bad_dtype(dtype)) return set_error(UNO_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (N < 0 || V < 1) return set_error(UNO_ERR_INVALID_ARG, "need N >= 0 and V >= 1");
+    if (!(temperature > 0.f) || !(temperature < INFINITY))
+        return set_error(UNO_ERR_INVALID_ARG, "temperature must be positive and finite");
+    if (temperature < 1e-30f) return set_error(UNO_ERR_UNSUPPORTED, "temperature >= 1e-30 is supported");
+    if (V > 0x7FFFF000) return set_error(UNO_ERR_UNSUPPORTED, "V < 2^31 - 4096 is supported");
+    if (N > 0x7FFFFFFF || (double)N * (double)V >= 1099511627776.0)
+        return set_error(UNO_ERR_UNSUPPORTED, "N < 2^31 and N * V < 2^40 are supported");
+    return UNO_OK;
+}
+
+}  // namespace
+}  // namespace uno
+
+extern "C" uno_status uno_token_logprobs(const void* logits, uno_dtype dtype, int64_t N, int64_t V, float temperature,
+                                         const int32_t* tokens, int32_t top_n, float* out_logprob, float* out_entropy,
+                                         float* out_stats, int32_t* out_top_ids, float* out_top_logprobs,
+                                         uno_stream_t stream) {
+    using namespace uno;
+    uno_status s = check_rows(dtype, N, V, temperature);
+    if (s != UNO_OK) return s;
+    if (top_n < 0) return set_error(UNO_ERR_INVALID_ARG, "top_n must be >= 0");
+    if (top_n > kMaxTop) return set_error(UNO_ERR_UNSUPPORTED, "top_n <= %d is supported", kMaxTop);
+    if (N == 0) return UNO_OK;
+    if (!logits) return set_error(UNO_ERR_INVALID_ARG, "logits is NULL");
+    if (out_logprob && !tokens) return set_error(UNO_ERR_INVALID_ARG, "out_logprob needs tokens");
+    if ((top_n > 0) != (out_top_ids != nullptr) || (top_n > 0) != (out_top_logprobs != nullptr))
+        return set_error(UNO_ERR_INVALID_ARG, "out_top_ids and out_top_logprobs are given exactly when top_n > 0");
+    if (!out_logprob && !out_entropy && !out_stats && !out_top_ids)
+        return set_error(UNO_ERR_INVALID_ARG, "at least one output is required");
+    const void* ptrs[] = {logits, tokens, out_logprob, out_entropy, out_stats, out_top_ids, out_top_logprobs};
+    for (const void* p : ptrs)
+        if (off16(p)) return set_error(UNO_ERR_UNSUPPORTED, "tensor pointers must be 16-byte aligned");
+    const Args a{V, (float)(1.4426950408889634 / (double)temperature), 1.0f / temperature, tokens, top_n,
+                 out_logprob, out_entropy, out_stats, out_top_ids, out_top_logprobs};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == UNO_F32 ? logprobs_launch<float>(logits, N, a, st) : logprobs_launch<__nv_bfloat16>(logits, N, a, st);
+}
+
+extern "C" uno_status uno_token_logprobs_grad(const void* logits, uno_dtype dtype, int64_t N, int64_t V,
+                                              float temperature, const int32_t* tokens, const float* stats,
+                                              const float* entropy, const float* grad_logprob,
+                                              const float* grad_entropy, void* grad_logits, uno_stream_t stream) {
+    using namespace uno;
+    uno_status s = check_rows(dtype, N, V, temperature);
+    if (s != UNO_OK) return s;
+    if (N == 0) return UNO_OK;
+    if (!logits || !stats || !grad_logits)
+        return set_error(UNO_ERR_INVALID_ARG, "logits, stats and grad_logits are required");
+    if (!grad_logprob && !grad_entropy)
+        return set_error(UNO_ERR_INVALID_ARG, "grad_logprob or grad_entropy is required");
+    if (grad_logprob && !tokens) return set_error(UNO_ERR_INVALID_ARG, "grad_logprob needs tokens");
+    if (grad_entropy && !entropy) return set_error(UNO_ERR_INVALID_ARG, "grad_entropy needs entropy");
+    const void* ptrs[] = {logits, tokens, stats, entropy, grad_logprob, grad_entropy, grad_logits};
+    for (const void* p : ptrs)
+        if (off16(p)) return set_error(UNO_ERR_UNSUPPORTED, "tensor pointers must be 16-byte aligned");
+    const GradArgs a{V, (float)(1.4426950408889634 / (double)temperature), 1.0f / temperature, tokens, stats,
+                     entropy, grad_logprob, grad_entropy, 0};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == UNO_F32 ? grad_launch<float>(logits, grad_logits, N, a, st)
+                            : grad_launch<__nv_bfloat16>(logits, grad_logits, N, a, st);
+}

@@ -226,42 +226,51 @@ def uno_block_noise(clean_tokens, uniforms, V, noised_tokens, row_gate=None, str
 
 # ---------------------------------------------------------------------------------------
 # include/uno_layers.h: every tensor's shape, dtype and device is checked here, and the call
-# runs on the tensors' device whichever one is current.
-_F8 = torch.float8_e4m3fn
-_FLOATS = (torch.bfloat16, torch.float32)
+# runs on the tensors' device whichever one is current. The checks stand on the path of every
+# small call: they compare first and look for what to say only where a comparison fails.
+_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+_CODES = {torch.bfloat16: UNO_BF16, torch.float32: UNO_F32}
 
 
-def _arg(name, t, shape, dtype, device):
-    """Device address of tensor `t` (None passes NULL) after checking what it has to be."""
+def _arg(name, t, shape, dtype, index):
+    """Device address of tensor `t` (None passes NULL) after checking what it has to be:
+    contiguous, of this shape and dtype, on CUDA device `index`."""
     if t is None:
         return None
-    p = _ptr(t)
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    return p
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t)
+    raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{index}, "
+                     f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 def _matrix(name, t, dtypes):
-    _ptr(t)
-    if t is None or t.dim() != 2:
+    """Shape of a matrix of one of the dtypes, on a CUDA device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        _ptr(t)
         raise ValueError(f"{name}: expected a matrix")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
     return t.shape
 
 
-def _call(fn, device, stream, *args):
-    """One library call on `device`, enqueued on `stream` (default: the device's current one)."""
+def _call(fn, index, stream, *args):
+    """One library call on CUDA device `index`, enqueued on `stream` (default: that device's
+    current one)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream))
+        stream = torch.cuda.current_stream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream))
+        with torch.cuda.device(index):
+            status = fn(*args, stream.cuda_stream)
+    if status != UNO_OK:
+        _check(status)
 
 
 def _blocks(n: int) -> int:
@@ -272,22 +281,22 @@ def uno_rms_norm_fp8(x, weight, eps, out_q=None, out_scale=None, residual=None, 
                      stream=None):
     """RMS norm of x (+ residual) with e4m3 values and a scale per 128 columns, and / or the
     norm in x's dtype (see include/uno_layers.h)."""
-    M, d = _matrix("x", x, _FLOATS)
-    dev, t = x.device, x.dtype
-    _call(load().uno_rms_norm_fp8, dev, stream, _ptr(x), _arg("residual", residual, (M, d), t, dev),
-          _arg("weight", weight, (d,), t, dev), _dtype_code(x), M, d, float(eps),
-          _arg("out_residual", out_residual, (M, d), t, dev), _arg("out_q", out_q, (M, d), _F8, dev),
-          _arg("out_scale", out_scale, (M, _blocks(d)), torch.float32, dev), _arg("out_y", out_y, (M, d), t, dev))
+    shape = M, d = _matrix("x", x, _CODES)
+    i, t = x.get_device(), x.dtype
+    _call(load().uno_rms_norm_fp8, i, stream, _arg("x", x, shape, t, i), _arg("residual", residual, shape, t, i),
+          _arg("weight", weight, (d,), t, i), _CODES[t], M, d, eps,
+          _arg("out_residual", out_residual, shape, t, i), _arg("out_q", out_q, shape, _F8, i),
+          _arg("out_scale", out_scale, (M, _blocks(d)), _F32, i), _arg("out_y", out_y, shape, t, i))
 
 
 def uno_fp8_quantize(x, out_q, out_scale, block_rows=1, stream=None):
     """e4m3 values and scales of x by block_rows x 128 blocks, block_rows 1 (activations) or
     128 (weights) (see include/uno_layers.h)."""
-    M, d = _matrix("x", x, _FLOATS)
-    dev, rows = x.device, int(block_rows)
-    _call(load().uno_fp8_quantize, dev, stream, _ptr(x), _dtype_code(x), M, d, rows,
-          _arg("out_q", out_q, (M, d), _F8, dev),
-          _arg("out_scale", out_scale, (M if rows == 1 else _blocks(M), _blocks(d)), torch.float32, dev))
+    shape = M, d = _matrix("x", x, _CODES)
+    i, t = x.get_device(), x.dtype
+    _call(load().uno_fp8_quantize, i, stream, _arg("x", x, shape, t, i), _CODES[t], M, d, block_rows,
+          _arg("out_q", out_q, shape, _F8, i),
+          _arg("out_scale", out_scale, (M if block_rows == 1 else _blocks(M), _blocks(d)), _F32, i))
 
 
 def uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank) -> int:
@@ -298,26 +307,26 @@ def uno_fp8_gated_lora_linear(x_q, x_scale, w_q, w_scale, y, x=None, lora_a=None
                               scale=1.0, workspace=None, stream=None):
     """y = (x_q x_scale)(w_q w_scale)^T + scale * diag(row_gate) (x lora_a^T) lora_b^T, the
     adapter only where lora_a is given (see include/uno_layers.h)."""
-    M, d_in = _matrix("x_q", x_q, (_F8,))
+    M, d_in = x_shape = _matrix("x_q", x_q, (_F8,))
     d_out = _matrix("w_q", w_q, (_F8,))[0]
-    dev, bf, f32 = x_q.device, torch.bfloat16, torch.float32
+    _matrix("y", y, _CODES)
+    i, bf = x_q.get_device(), torch.bfloat16
     rank = 0 if lora_a is None else _matrix("lora_a", lora_a, (bf,))[0]
-    _matrix("y", y, _FLOATS)
     ws, nb = None, 0
     if rank:
-        nb = uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank)
         made = workspace is None
-        ws, nb = _workspace(nb, dev, workspace)
-        if ws is not None and ws.device != dev:
-            raise ValueError(f"workspace is on {ws.device}, the tensors are on {dev}")
+        ws, nb = _workspace(uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank), x_q.device, workspace)
+        if ws is not None and ws.get_device() != i:
+            raise ValueError(f"workspace is on {ws.device}, the tensors are on cuda:{i}")
         if made and ws is not None and stream is not None:
             ws.record_stream(stream)  # it may not be handed out again before this stream is done with it
-    _call(load().uno_fp8_gated_lora_linear, dev, stream, _ptr(x_q),
-          _arg("x_scale", x_scale, (M, _blocks(d_in)), f32, dev), _arg("w_q", w_q, (d_out, d_in), _F8, dev),
-          _arg("w_scale", w_scale, (_blocks(d_out), _blocks(d_in)), f32, dev), _arg("x", x, (M, d_in), bf, dev),
-          _arg("lora_a", lora_a, (rank, d_in), bf, dev), _arg("lora_b", lora_b, (d_out, rank), bf, dev),
-          _arg("row_gate", row_gate, (M,), f32, dev), float(scale), M, d_in, d_out, rank,
-          _arg("y", y, (M, d_out), y.dtype, dev), _dtype_code(y), _ptr(ws), nb)
+        ws = _ptr(ws)
+    _call(load().uno_fp8_gated_lora_linear, i, stream, _arg("x_q", x_q, x_shape, _F8, i),
+          _arg("x_scale", x_scale, (M, _blocks(d_in)), _F32, i), _arg("w_q", w_q, (d_out, d_in), _F8, i),
+          _arg("w_scale", w_scale, (_blocks(d_out), _blocks(d_in)), _F32, i), _arg("x", x, x_shape, bf, i),
+          _arg("lora_a", lora_a, (rank, d_in), bf, i), _arg("lora_b", lora_b, (d_out, rank), bf, i),
+          _arg("row_gate", row_gate, (M,), _F32, i), scale, M, d_in, d_out, rank,
+          _arg("y", y, (M, d_out), y.dtype, i), _CODES[y.dtype], ws, nb)
     return y
 
 
@@ -326,24 +335,25 @@ def uno_token_logprobs(logits, tokens, out_logprob=None, temperature=1.0, out_en
     """Log probability of each row's token, entropy, the most probable tokens (as many as
     out_top_ids has columns), and the statistics the gradient needs; rows whose token is not
     in [0, V) are left out (see include/uno_layers.h)."""
-    N, V = _matrix("logits", logits, _FLOATS)
-    dev, f32, i32 = logits.device, torch.float32, torch.int32
-    top = 0 if out_top_ids is None else _matrix("out_top_ids", out_top_ids, (i32,))[1]
-    _call(load().uno_token_logprobs, dev, stream, _ptr(logits), _dtype_code(logits), N, V, float(temperature),
-          _arg("tokens", tokens, (N,), i32, dev), top, _arg("out_logprob", out_logprob, (N,), f32, dev),
-          _arg("out_entropy", out_entropy, (N,), f32, dev), _arg("out_stats", out_stats, (N, 2), f32, dev),
-          _arg("out_top_ids", out_top_ids, (N, top), i32, dev) if top else None,
-          _arg("out_top_logprobs", out_top_logprobs, (N, top), f32, dev) if top else None)
+    shape = N, V = _matrix("logits", logits, _CODES)
+    i, t = logits.get_device(), logits.dtype
+    k = 0 if out_top_ids is None else _matrix("out_top_ids", out_top_ids, (_I32,))[1]
+    ids = lps = None
+    if k:
+        ids, lps = _arg("out_top_ids", out_top_ids, (N, k), _I32, i), \
+            _arg("out_top_logprobs", out_top_logprobs, (N, k), _F32, i)
+    _call(load().uno_token_logprobs, i, stream, _arg("logits", logits, shape, t, i), _CODES[t], N, V, temperature,
+          _arg("tokens", tokens, (N,), _I32, i), k, _arg("out_logprob", out_logprob, (N,), _F32, i),
+          _arg("out_entropy", out_entropy, (N,), _F32, i), _arg("out_stats", out_stats, (N, 2), _F32, i), ids, lps)
 
 
 def uno_token_logprobs_grad(logits, tokens, stats, grad_logits, grad_logprob=None, entropy=None, grad_entropy=None,
                             temperature=1.0, stream=None):
     """Gradient of uno_token_logprobs' log probabilities and entropies with respect to the
     logits; grad_logits may be logits itself (see include/uno_layers.h)."""
-    N, V = _matrix("logits", logits, _FLOATS)
-    dev, f32 = logits.device, torch.float32
-    _call(load().uno_token_logprobs_grad, dev, stream, _ptr(logits), _dtype_code(logits), N, V, float(temperature),
-          _arg("tokens", tokens, (N,), torch.int32, dev), _arg("stats", stats, (N, 2), f32, dev),
-          _arg("entropy", entropy, (N,), f32, dev), _arg("grad_logprob", grad_logprob, (N,), f32, dev),
-          _arg("grad_entropy", grad_entropy, (N,), f32, dev),
-          _arg("grad_logits", grad_logits, (N, V), logits.dtype, dev))
+    shape = N, V = _matrix("logits", logits, _CODES)
+    i, t = logits.get_device(), logits.dtype
+    _call(load().uno_token_logprobs_grad, i, stream, _arg("logits", logits, shape, t, i), _CODES[t], N, V, temperature,
+          _arg("tokens", tokens, (N,), _I32, i), _arg("stats", stats, (N, 2), _F32, i),
+          _arg("entropy", entropy, (N,), _F32, i), _arg("grad_logprob", grad_logprob, (N,), _F32, i),
+          _arg("grad_entropy", grad_entropy, (N,), _F32, i), _arg("grad_logits", grad_logits, shape, t, i))

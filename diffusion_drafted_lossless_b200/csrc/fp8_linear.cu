@@ -11,16 +11,23 @@
 // nothing. T is made by the same kernel first: a product with adapter blocks alone (X, A) and
 // factor 1.
 //
-// A CTA computes a 128 x BN tile (or, in a cluster of S CTAs, its share of the tile's K
-// blocks). Warp 0 loads K blocks by TMA into a ring of shared-memory stages; warp 1 issues
-// tcgen05.mma into one of NB accumulators; eight epilogue warps (two for each quarter of the
-// 128 TMEM lanes, half of the columns each) drain them. The sums then pass through shared
-// memory, where the CTAs of a cluster add theirs up in rank order (distributed shared
-// memory), and leave as whole rows. Rows past M are never stored; a small M shrinks the
-// loaded rows of x, not the product.
+// Roles of a CTA's warps: 0 loads K blocks by TMA into a ring of shared-memory stages; 1 and 2
+// issue tcgen05.mma for the even and the odd K blocks, each into accumulators of its own
+// (waiting, issuing and committing a K block takes a warp about as long as its product); 3
+// brings the factors into shared memory, eight K blocks ahead; the others, four for each
+// column group, one for each quarter of the 128 TMEM lanes, drain the accumulators.
+// What set this shape, measured on 128 x 256 tiles in clocks per K block (its product takes
+// 512): 1900 with a release at cluster scope on the way back to the products; 1530 with each
+// thread loading its own row's scale (32 lines an instruction, in the array that the products
+// read their operands from); 1480 with TMEM reads, waits and additions in turn; ~1000 of them
+// for a barrier of all drains around the staging of scales.
 //
-// Two CTAs fit on an SM (shared memory, TMEM and registers are sized for it): one's prologue,
-// drain and stores overlap the other's product.
+// Two forms:
+//   wide (large products): 128 x 256 tiles, one CTA per SM, persistent, sixteen draining warps
+//   narrow: 128 x 128 or 128 x 64 tiles, two CTAs per SM, eight draining warps; a cluster of S
+//     CTAs shares a tile's K blocks where there are few tiles, and adds its sums up through
+//     distributed shared memory, in rank order
+// Rows past M are never stored; a small M shrinks the loaded rows of x, not the product.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -33,18 +40,17 @@ namespace uno {
 namespace fp8lin {
 
 constexpr int BM = 128;
-constexpr int kRowBytes = 128;  // bytes of a K block's row: one 128-byte swizzle row
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kRowBytes = 128;       // bytes of a K block's row: one 128-byte swizzle row
+constexpr int kRoles = 4;            // warps before the draining ones
 constexpr int kMaxStages = 8;
-constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
-constexpr int kSmemLeast = 78 * 1024;   // and never three: the third's wait for TMEM could hold up a cluster
-constexpr int kTmemCols = 256;          // of 512: two CTAs per SM
+constexpr int kMaxSplit = 8;         // CTAs that share a tile's K blocks
+constexpr int kChunk = 8;            // K blocks whose factors are staged together
+constexpr int kFactorPitch = BM + 4; // floats of a K block's factors (writes on 32 banks)
 
 struct Params {
     int M, N;              // rows and columns of Y
     int nk8, nk16;         // K blocks of e4m3 and of bf16
-    int m_tiles;
+    int m_tiles, tiles;    // row tiles, all tiles
     int stages;
     uint32_t a_rows;       // rows of x loaded per K block (a multiple of 8, at most 128)
     const float* xs;       // [M, nk8]
@@ -102,16 +108,63 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&r)[32]) {
+// R columns of this warp's 32 lanes, without waiting; tmem_wait makes them usable (it names
+// them, so that no use is moved ahead of it)
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])
+                 :
+                 : "memory");
+}
+
+// True in one lane of a converged warp. The roles below run whole warps and issue under this
+// predicate: the compiler then keeps descriptors and addresses in uniform registers, which a
+// branch on the lane number denies it (a K block's four products issue in 150 clocks instead
+// of 400, and a wait for a phase that is over takes 115 instead of 320).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// Arrive without release semantics: what is handed over is a TMEM accumulator whose reads
+// have completed (tcgen05.wait::ld), no memory. A release at cluster scope costs more than
+// a thousand clocks.
+__device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
-          "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
-          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr)
         : "memory");
 }
@@ -149,49 +202,202 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
     return false;
 }
 
-template <int BN>
-__global__ void __launch_bounds__(kThreads, 2)
+// Two phases at once: their first polls are in flight together
+__device__ __forceinline__ bool wait_phases(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* gave_up) {
+    const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+    return (ra || wait_phase(a, pa, gave_up)) && (rb || wait_phase(b, pb, gave_up));
+}
+
+// two columns of a row's float32 sums in a register pair
+__device__ __forceinline__ float2 columns(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+
+// acc[at / 2 ..] += f * r
+template <int N, int R>
+__device__ __forceinline__ void add_scaled(uint64_t (&acc)[N], int at, float f, const float (&r)[R]) {
+    const uint64_t ff = pair_of(f, f);
+#pragma unroll
+    for (int j = 0; j < R / 2; ++j)
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[at / 2 + j]) : "l"(ff), "l"(pair_of(r[2 * j], r[2 * j + 1])));
+}
+
+// ---------------------------------------------------------------------------------------
+// stores: a draining thread holds columns of one row; a warp's store instruction should write
+// whole lines. Eight lanes exchange 16-byte chunks (a transposition in three steps), after
+// which lane j of the eight holds chunk j of each of their rows.
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ void exchange(uint4 (&v)[8], int lane) {
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k & d) continue;
+            uint4 give = up ? v[k] : v[k | d], got;
+            got.x = __shfl_xor_sync(kFullMask, give.x, d);
+            got.y = __shfl_xor_sync(kFullMask, give.y, d);
+            got.z = __shfl_xor_sync(kFullMask, give.z, d);
+            got.w = __shfl_xor_sync(kFullMask, give.w, d);
+            if (up) v[k] = got;
+            else v[k | d] = got;
+        }
+    }
+}
+
+// CW columns from `col` on of rows row0 + lane (this warp's 32 rows)
+template <int CW>
+__device__ __forceinline__ void store_rows(const Params& p, int row0, int col, int lane, const uint64_t (&acc)[CW / 2]) {
+    if (!p.y_f32 && p.N % 8 == 0) {  // rows of bf16 that start on 16 bytes: by whole lines
+        constexpr int K = CW / 8;    // chunks of 8 columns: eight, or four
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k < K) {
+                const float2 a = columns(acc[4 * k % (CW / 2)]), b = columns(acc[(4 * k + 1) % (CW / 2)]),
+                             c = columns(acc[(4 * k + 2) % (CW / 2)]), d = columns(acc[(4 * k + 3) % (CW / 2)]);
+                v[k] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(c.x, c.y), pack_bf16(d.x, d.y));
+            } else {
+                v[k] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        exchange(v, lane);
+        const int j = lane & 7, r0 = row0 + (lane & ~7), c0 = col + 8 * j;
+        const bool in = j < K && c0 < p.N;
+        char* y = static_cast<char*>(p.y) + ((int64_t)r0 * p.N + c0) * 2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (in && r0 + i < p.M) *reinterpret_cast<uint4*>(y) = v[i];
+            y += (int64_t)p.N * 2;
+        }
+    } else {
+        const int row = row0 + lane, n = row < p.M ? p.N - col : 0;  // columns of this row that exist
+        const int64_t o = (int64_t)row * p.N + col;
+        float* yf = static_cast<float*>(p.y) + o;
+        __nv_bfloat16* yb = static_cast<__nv_bfloat16*>(p.y) + o;
+#pragma unroll
+        for (int j = 0; j < CW; j += 4) {
+            const float2 a = columns(acc[j / 2]), b = columns(acc[j / 2 + 1]);
+            if (p.y_f32 && p.N % 4 == 0) {
+                if (j < n) *reinterpret_cast<float4*>(yf + j) = make_float4(a.x, a.y, b.x, b.y);
+            } else if (p.y_f32) {
+                if (j < n) yf[j] = a.x;
+                if (j + 1 < n) yf[j + 1] = a.y;
+                if (j + 2 < n) yf[j + 2] = b.x;
+                if (j + 3 < n) yf[j + 3] = b.y;
+            } else {
+                if (j < n) yb[j] = __float2bfloat16_rn(a.x);
+                if (j + 1 < n) yb[j + 1] = __float2bfloat16_rn(a.y);
+                if (j + 2 < n) yb[j + 2] = __float2bfloat16_rn(b.x);
+                if (j + 3 < n) yb[j + 3] = __float2bfloat16_rn(b.y);
+            }
+        }
+    }
+}
+
+// four columns of a row
+__device__ __forceinline__ void store4(const Params& p, int64_t row, int col, const float4& v) {
+    const int64_t o = row * p.N + col;
+    const float w[4] = {v.x, v.y, v.z, v.w};
+    if (p.y_f32) {
+        float* y = static_cast<float*>(p.y) + o;
+        if (p.N % 4 == 0) {
+            *reinterpret_cast<float4*>(y) = v;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col + j < p.N) y[j] = w[j];
+        }
+    } else {
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + o;
+        if (p.N % 4 == 0) {
+            *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col + j < p.N) y[j] = __float2bfloat16_rn(w[j]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// BN: columns of a tile; EW: draining warps; CTAS: CTAs per SM that registers, TMEM and shared
+// memory are sized for. NB accumulators of BN columns share the CTA's 512 / CTAS of TMEM.
+// ---------------------------------------------------------------------------------------
+template <int BN, int EW, int CTAS>
+struct Form {
+    static constexpr int bn = BN, threads = 32 * (kRoles + EW), ctas = CTAS;
+    static constexpr int CW = BN * 4 / EW;                     // columns of a draining warp
+    static constexpr int C = CTAS == 1 ? 16 : 8;               // columns read ahead (as registers allow)
+    static constexpr int tmem = 512 / CTAS, NB = tmem / BN;
+    static constexpr int halves = BN > kBlockCols ? BN / kBlockCols : 1;  // blocks of weight rows
+    // registers a thread at launch, and after the split: the role warps give up theirs. The
+    // split's sum may not exceed the launch's total.
+    static constexpr int regs = CTAS == 1 ? 96 : 80, role_regs = 32, drain_regs = CTAS == 1 ? 112 : 104;
+    static_assert(32 * kRoles * role_regs + 32 * EW * drain_regs <= threads * regs, "register split");
+    static constexpr int factor_bytes = 2 * halves * kChunk * kFactorPitch * 4;
+    // dynamic shared memory: the SM's 227 KB (1 KB less for each CTA) without the static part
+    static constexpr int smem = (CTAS == 1 ? 226 * 1024 : 112 * 1024) - factor_bytes - 512;
+};
+using Wide = Form<256, 16, 1>;
+using Narrow128 = Form<128, 8, 2>;
+using Narrow64 = Form<64, 8, 2>;
+
+template <class F>
+__global__ void __launch_bounds__(F::threads, F::ctas)
 linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CUtensorMap tW,
               const __grid_constant__ CUtensorMap tT, const __grid_constant__ CUtensorMap tB, const Params p) {
-    constexpr int NB = kTmemCols / BN;  // accumulators
-    constexpr int CW = BN / 2;          // columns of an epilogue warp
-    constexpr int PITCH = BN + 4;       // floats of a row of sums in shared memory (no bank conflicts)
+    constexpr int BN = F::bn, CW = F::CW, C = F::C, NB = F::NB, EW = F::threads / 32 - kRoles;
+    constexpr int PITCH = BN + 4;  // floats of a row of sums in shared memory (no bank conflicts)
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[NB], tempty[NB], drain;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[NB], tempty[NB], sfull[2], sempty[2],
+        drain[2];
+    __shared__ float factors[2][F::halves][kChunk][kFactorPitch];
     __shared__ uint32_t tmem_base;
     __shared__ int s_gave_up;
 
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
-    const int ST = p.stages;
+    const uint32_t ST = (uint32_t)p.stages;
     const uint32_t a_bytes = p.a_rows * kRowBytes;
     constexpr uint32_t b_bytes = BN * kRowBytes;
-    const uint32_t ring_b = ring + (uint32_t)ST * a_bytes;
+    const uint32_t ring_b = ring + ST * a_bytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* gave_up = &s_gave_up;
-    const uint32_t S = cluster_size(), rank = cluster_rank();
-    const int tile = blockIdx.x / S;
-    const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
-    // this CTA's share of the K blocks
+    const uint32_t S = F::ctas == 1 ? 1u : cluster_size(), rank = F::ctas == 1 ? 0u : cluster_rank();
+    const int tile0 = blockIdx.x / S, step = gridDim.x / S;
+    // this CTA's share of the K blocks of its tiles
     const int nk = p.nk8 + p.nk16;
     const int kb0 = (int)((int64_t)nk * rank / S), kb1 = (int)((int64_t)nk * (rank + 1) / S);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < ST; ++s) {
+        for (uint32_t s = 0; s < ST; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < NB; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kEpiWarps);
+            mbar_init(&tempty[b], EW);
         }
-        mbar_init(&drain, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sfull[b], 1);
+            mbar_init(&sempty[b], EW);
+            mbar_init(&drain[b], 1);
+        }
         s_gave_up = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
-                     "n"(kTmemCols)
+                     "n"(F::tmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -203,12 +409,14 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     // before it reads what this one writes)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    float acc[CW];
+    if (warp < kRoles) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::role_regs));
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, got = 0;
-            uint32_t ph = 1;
-            bool waited = !p.wait_t;
+        const bool one = elect_one();
+        uint32_t s = 0, ph = 1, got = 0;
+        bool waited = !p.wait_t;
+        for (int tile = tile0; tile < p.tiles && !*gave_up; tile += step) {
+            const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
             for (int kb = kb0; kb < kb1; ++kb, ++got) {
                 if (got >= ST && !wait_phase(&empty[s], ph, gave_up)) {
                     *gave_up = 1;
@@ -219,38 +427,47 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                     asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;" ::: "memory");
                     waited = true;
                 }
-                mbar_arrive_expect_tx(&full[s], a_bytes + b_bytes);
-                const uint32_t a = ring + (uint32_t)s * a_bytes, b = ring_b + (uint32_t)s * b_bytes;
-                if (low) {
-                    load_2d(a, &tT, (kb - p.nk8) * 64, m0, &full[s]);
-                    load_2d(b, &tB, (kb - p.nk8) * 64, n0, &full[s]);
-                } else {
-                    load_2d(a, &tX, kb * 128, m0, &full[s]);
-                    load_2d(b, &tW, kb * 128, n0, &full[s]);
+                if (one) {
+                    mbar_arrive_expect_tx(&full[s], a_bytes + b_bytes);
+                    const uint32_t a = ring + s * a_bytes, b = ring_b + s * b_bytes;
+                    if (low) {
+                        load_2d(a, &tT, (kb - p.nk8) * 64, m0, &full[s]);
+                        load_2d(b, &tB, (kb - p.nk8) * 64, n0, &full[s]);
+                    } else {
+                        load_2d(a, &tX, kb * 128, m0, &full[s]);
+                        load_2d(b, &tW, kb * 128, n0, &full[s]);
+                    }
                 }
                 if (++s == ST) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
-            if (*gave_up)  // loads that no product will read: let them land
-                for (int j = got > ST ? got - ST : 0; j < got; ++j) mbar_wait(&full[j % ST], (j / ST) & 1, 1u << 16);
+            __syncwarp();
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint64_t da0 = operand_desc(ring), db0 = operand_desc(ring_b);
-            int s = 0, b = 0;
-            uint32_t ph = 0, bph = 1;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if ((kb - kb0 >= NB && !wait_phase(&tempty[b], bph, gave_up)) || !wait_phase(&full[s], ph, gave_up)) {
-                    *gave_up = 1;
-                    break;
-                }
-                fence_after();
-                const uint64_t da = da0 + (uint64_t)(((uint32_t)s * a_bytes) >> 4);
-                const uint64_t db = db0 + (uint64_t)(((uint32_t)s * b_bytes) >> 4);
-                const uint32_t d = tmem + (uint32_t)(b * BN);
-                if (kb < p.nk8) {
+        if (*gave_up)  // loads that no product will read: let them land
+            for (uint32_t j = got > ST ? got - ST : 0; j < got; ++j) mbar_wait(&full[j % ST], (j / ST) & 1, 1u << 16);
+        __syncwarp();
+    } else if (warp <= 2) {
+        // K block i of the CTA goes to accumulator i mod NB (NB is even)
+        const bool one = elect_one();
+        const uint64_t da0 = operand_desc(ring), db0 = operand_desc(ring_b);
+        const uint32_t odd = (uint32_t)warp - 1u, nkl = (uint32_t)(kb1 - kb0);
+        const uint32_t mine = p.tiles > tile0 ? (uint32_t)((p.tiles - 1 - tile0) / step + 1) : 0u;
+        uint32_t b = odd, bph = 1, s = odd % ST, ph = (odd / ST) & 1u;
+        uint32_t kl = nkl ? odd % nkl : 0;
+        for (uint32_t i = odd; i < mine * nkl; i += 2) {
+            const bool ok = i < (uint32_t)NB ? wait_phase(&full[s], ph, gave_up)
+                                             : wait_phases(&full[s], ph, &tempty[b], bph, gave_up);
+            if (!ok) {
+                *gave_up = 1;
+                break;
+            }
+            fence_after();
+            if (one) {
+                const uint64_t da = da0 + (uint64_t)((s * a_bytes) >> 4), db = db0 + (uint64_t)((s * b_bytes) >> 4);
+                const uint32_t d = tmem + b * BN;
+                if (kb0 + (int)kl < p.nk8) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // 32 bytes of K per instruction
                         mma_e4m3(d, da + 2 * k, db + 2 * k, idesc_e4m3(BM, BN), k > 0);
@@ -258,134 +475,187 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mma_bf16(d, da + 2 * k, db + 2 * k, idesc_bf16(BM, BN), k > 0);
                 }
-                commit(&empty[s]);
                 commit(&tfull[b]);
-                if (++s == ST) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-                if (++b == NB) {
-                    b = 0;
-                    bph ^= 1u;
-                }
+                commit(&empty[s]);
             }
-            if (*gave_up) {  // products in flight end before their memory is given back
-                commit(&drain);
-                mbar_wait(&drain, 0, 1u << 16);
+            s += 2;
+            if (s >= ST) {
+                s -= ST;
+                ph ^= 1u;
+            }
+            b += 2;
+            if (b >= (uint32_t)NB) {
+                b -= NB;
+                bph ^= 1u;
+            }
+            for (kl += 2; kl >= nkl;) kl -= nkl;
+        }
+        __syncwarp();
+        if (*gave_up) {  // products in flight end before their memory is given back
+            if (one) commit(&drain[odd]);
+            mbar_wait(&drain[odd], 0, 1u << 16);
+        }
+        __syncwarp();
+    } else {
+        // factors[..][half][k][row] of the next eight K blocks: a row's scales of eight K blocks
+        // are one 32-byte sector, read once for the tile
+        uint32_t cb = 0, ph = 1, chunks = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < p.tiles && ok; tile += step) {
+            const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
+            for (int kc = kb0; kc < kb1; kc += kChunk, ++chunks) {
+                // this lane's K block kb = kc + lane % 8, rows lane / 8, + 4, + 8, ...
+                const int kb = kc + (lane & (kChunk - 1)), row = m0 + lane / kChunk;
+                const bool low = kb >= p.nk8;
+                const float* src = low ? p.gate : p.xs;
+                const int step_row = low ? 1 : p.nk8;
+                if (src) src += low ? row : (int64_t)row * p.nk8 + kb;
+                float mul[F::halves];
+#pragma unroll
+                for (int h = 0; h < F::halves; ++h) {
+                    const int n = n0 + h * kBlockCols;
+                    mul[h] = kb >= kb1 || n >= p.N ? 0.f
+                             : !low                ? __ldg(p.ws + (int64_t)(n / kBlockCols) * p.nk8 + kb)
+                             : p.gate              ? p.scale
+                                                   : 1.f;
+                }
+                if (chunks >= 2) ok = wait_phase(&sempty[cb], ph, gave_up);
+                if (!ok) {
+                    *gave_up = 1;
+                    break;
+                }
+                float* dst = &factors[cb][0][lane & (kChunk - 1)][lane / kChunk];
+#pragma unroll 1
+                for (int r = 0; r < BM && row + r < p.M; r += 16, dst += 16) {
+                    float x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = row + r + 4 * j >= p.M ? 0.f : src ? __ldg(src + (int64_t)(r + 4 * j) * step_row) : 1.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int h = 0; h < F::halves; ++h) dst[h * kChunk * kFactorPitch + 4 * j] = x[j] * mul[h];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfull[cb]);
+                cb ^= 1u;
+                if (cb == 0) ph ^= 1u;
             }
         }
+        __syncwarp();
+    }
     } else {
-        // ---- epilogue: acc += factor * accumulator, one row a thread, CW columns ----
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        const int row = m0 + quarter * 32 + lane;
-        const bool any = m0 + quarter * 32 < p.M;  // (a warp of rows past M only keeps the barriers going)
-        const float* xs = p.xs + (int64_t)(row < p.M ? row : 0) * p.nk8;
-        const float* ws = p.ws + (int64_t)(n0 / kBlockCols) * p.nk8;
-        const float low = p.gate ? (row < p.M ? p.scale * p.gate[row] : 0.f) : 1.f;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::drain_regs));
+        // ---- draining: acc += factor * accumulator, one row a thread, CW columns. C columns are
+        // read ahead of those being added up, across K blocks too. ----
+        const int quarter = warp & 3, group = (warp - kRoles) >> 2, r0 = quarter * 32;
+        const uint32_t taddr = tmem + (uint32_t)(group * CW) + ((uint32_t)r0 << 16);
+        uint32_t b = 0, bph = 0, cb = 0, sph = 0;
+        bool ok = true;
+        uint64_t acc[CW / 2];  // (column pairs of one row)
+        for (int tile = tile0; tile < p.tiles && ok; tile += step) {
+            const int m0 = (tile % p.m_tiles) * BM, col = (tile / p.m_tiles) * BN + group * CW;
+            const bool any = m0 + r0 < p.M;  // (a warp of rows past M only keeps the barriers going)
+            const float* fs = &factors[cb][F::halves > 1 ? group * CW / kBlockCols : 0][0][r0 + lane];
 #pragma unroll
-        for (int j = 0; j < CW; ++j) acc[j] = 0.f;
-        int b = 0;
-        uint32_t bph = 0;
-        float f4[4];
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const int at = (kb - kb0) & 3;
-            if (at == 0 && any) {  // the factors of the next four K blocks
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    f4[j] = kb + j < p.nk8 ? __ldg(xs + kb + j) * __ldg(ws + kb + j) : low;
-            }
-            if (!__all_sync(kFullMask, wait_phase(&tfull[b], bph, gave_up))) {
+            for (int j = 0; j < CW / 2; ++j) acc[j] = 0;
+            float r[2][C];
+            ok = __all_sync(kFullMask, wait_phase(&sfull[cb], sph, gave_up) && wait_phase(&tfull[b], bph, gave_up));
+            if (!ok) {
                 *gave_up = 1;
                 break;
             }
+            float f = *fs;
             fence_after();
-            if (any) {
-                const float f = at == 0 ? f4[0] : at == 1 ? f4[1] : at == 2 ? f4[2] : f4[3];
-                const bool off = kb >= p.nk8 && f == 0.f;  // no adapter on this row, whatever its product holds
-                const uint32_t taddr = tmem + (uint32_t)(b * BN + half * CW) + ((uint32_t)(quarter * 32) << 16);
+            if (any) tmem_load(taddr + b * BN, r[0]);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const float fk = f;
+                const bool off = kb >= p.nk8 && fk == 0.f;  // no adapter on this row, whatever its product holds
 #pragma unroll
-                for (int c = 0; c < CW; c += 32) {
-                    float r[32];
-                    __syncwarp();
-                    tmem_load32(taddr + (uint32_t)c, r);
-                    if (!off) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(f, r[j], acc[c + j]);
+                for (int c = 0; c < CW; c += C) {
+                    if (any) tmem_wait(r[c / C & 1]);
+                    if (c + C < CW) {
+                        if (any) tmem_load(taddr + b * BN + (uint32_t)(c + C), r[c / C + 1 & 1]);
+                    } else {
+                        // this accumulator is read and may be filled again; on to the next one
+                        fence_before();
+                        if (lane == 0) arrive_relaxed(&tempty[b]);
+                        if (++b == (uint32_t)NB) {
+                            b = 0;
+                            bph ^= 1u;
+                        }
+                        const int k = (kb + 1 - kb0) & (kChunk - 1);
+                        if (k == 0 || kb + 1 == kb1) {  // the chunk of factors is used up
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sempty[cb]);
+                            cb ^= 1u;
+                            if (cb == 0) sph ^= 1u;
+                            fs = &factors[cb][F::halves > 1 ? group * CW / kBlockCols : 0][0][r0 + lane];
+                        }
+                        if (kb + 1 < kb1) {
+                            bool there = wait_phase(&tfull[b], bph, gave_up);
+                            if (k == 0) there = there && wait_phase(&sfull[cb], sph, gave_up);
+                            ok = __all_sync(kFullMask, there);
+                            f = fs[k * kFactorPitch];
+                            fence_after();
+                            if (any && ok) tmem_load(taddr + b * BN, r[c / C + 1 & 1]);
+                        }
                     }
+                    if (any && !off) add_scaled(acc, c, fk, r[c / C & 1]);
+                    __syncwarp();
+                }
+                if (!ok) {
+                    *gave_up = 1;
+                    break;
                 }
             }
-            fence_before();
+            if (S == 1 && any && ok) store_rows<CW>(p, m0 + r0, col, lane, acc);
+        }
+        if (S > 1) {
+            // ---- the CTAs' sums through shared memory (the ring: this CTA's products, which this
+            // warp has seen end, were its last readers) ----
+            const int m0 = (tile0 % p.m_tiles) * BM, n0 = (tile0 / p.m_tiles) * BN;
+            const int rows = p.M - m0 < BM ? p.M - m0 : BM;
+            if (r0 + lane < rows) {
+                const uint32_t at = ring + (uint32_t)((r0 + lane) * PITCH + group * CW) * 4u;
+#pragma unroll
+                for (int j = 0; j < CW / 2; j += 2)
+                    asm volatile("st.shared.v2.b64 [%0], {%1,%2};" ::"r"(at + j * 8u), "l"(acc[j]), "l"(acc[j + 1])
+                                 : "memory");
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[b]);
-            if (++b == NB) {
-                b = 0;
-                bph ^= 1u;
+            cluster_sync();
+            // rank r of the cluster writes its share of the rows, four columns a thread
+            const int first = (int)(rows * rank / S), n = ((int)(rows * (rank + 1) / S) - first) * (BN / 4);
+            for (int i = threadIdx.x - 32 * kRoles; i < n && ok; i += 32 * EW) {
+                const int r = first + i / (BN / 4), c = (i % (BN / 4)) * 4;
+                if (n0 + c >= p.N) continue;
+                const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
+                float4 part[kMaxSplit];
+#pragma unroll
+                for (uint32_t k = 0; k < kMaxSplit; ++k)
+                    part[k] = k < S ? ld_cluster(at, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 v = part[0];
+#pragma unroll
+                for (uint32_t k = 1; k < kMaxSplit; ++k)
+                    v.x += part[k].x, v.y += part[k].y, v.z += part[k].z, v.w += part[k].w;
+                store4(p, m0 + r, n0 + c, v);
             }
         }
+        __syncwarp();
     }
 
-    // ---- the tile's sums, through shared memory (the ring: every product has read its stage) ----
+    if (S > 1) {
+        __syncwarp();
+        if (warp < kRoles) cluster_sync();  // (the draining warps' turn is above)
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its sums
+    }
     fence_before();
     __syncthreads();
     fence_after();
-    const int rows = p.M - m0 < BM ? p.M - m0 : BM;
-    if (warp >= 2) {
-        const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane;
-        if (r < rows) {
-            const uint32_t at = ring + (uint32_t)(r * PITCH + half * CW) * 4u;
-#pragma unroll
-            for (int j = 0; j < CW; j += 4)
-                asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at + j * 4u), "f"(acc[j]), "f"(acc[j + 1]),
-                             "f"(acc[j + 2]), "f"(acc[j + 3])
-                             : "memory");
-        }
-    }
-    __syncwarp();
-    if (S > 1) cluster_sync();
-    else __syncthreads();
-    if (!*gave_up) {
-        // rank r of the cluster writes its share of the rows
-        const int r0 = (int)(rows * rank / S), r1 = (int)(rows * (rank + 1) / S);
-        const bool vec = p.N % 8 == 0;  // rows start on 16 bytes
-        for (int i = threadIdx.x; i < (r1 - r0) * (BN / 8); i += kThreads) {
-            const int r = r0 + i / (BN / 8), c = (i % (BN / 8)) * 8;
-            const int col = n0 + c;
-            if (col >= p.N) continue;
-            float v[8] = {};
-            const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;
-            for (uint32_t k = 0; k < S; ++k) {
-                const float4 lo = ld_cluster(at, k), hi = ld_cluster(at + 16u, k);
-                v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
-                v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
-            }
-            const int64_t o = (int64_t)(m0 + r) * p.N + col;
-            if (p.y_f32) {
-                float* y = static_cast<float*>(p.y) + o;
-                if (vec) {
-                    reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + j < p.N) y[j] = v[j];
-                }
-            } else {
-                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + o;
-                if (vec) {
-                    *reinterpret_cast<uint4*>(y) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + j < p.N) y[j] = __float2bfloat16_rn(v[j]);
-                }
-            }
-        }
-    }
-    __syncwarp();
-    if (S > 1) cluster_sync();  // no CTA leaves while another reads its sums
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::tmem) : "memory");
     if (threadIdx.x == 0 && *gave_up) record_device_status(p.status, (uint32_t)UNO_ERR_TIMEOUT);
 }
 
@@ -423,56 +693,91 @@ uno_status operand_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t co
     return UNO_OK;
 }
 
+// How a product of M x N with nk K blocks is run
 struct Shape {
-    int BN, S, stages;
+    int BN;      // 256: the wide form
+    int S;       // CTAs per tile
+    int stages;
     uint32_t a_rows;
     size_t smem;
 };
 
-// Tile width, CTAs per tile and ring depth of a product of M x N with nk K blocks.
-Shape choose(int64_t M, int64_t N, int nk, int sms) {
+constexpr int64_t kWideTiles = 100;
+
+template <class F>
+Shape shape_of(int64_t M, int S) {
     Shape c{};
+    c.BN = F::bn;
+    c.S = S;
     c.a_rows = M >= BM ? BM : (uint32_t)((M + 7) / 8 * 8);
-    const int64_t m_tiles = (M + BM - 1) / BM;
-    c.BN = m_tiles * ((N + 127) / 128) * 8 < sms ? 64 : 128;
-    const int64_t tiles = m_tiles * ((N + c.BN - 1) / c.BN);
-    c.S = 1;
-    while (c.S < 8 && tiles * c.S * 2 <= 2 * sms && nk >= c.S * 4) c.S *= 2;
-    const uint32_t stage = (c.a_rows + c.BN) * kRowBytes;
-    const uint32_t sums = BM * (uint32_t)(c.BN + 4) * 4u;
-    c.stages = (int)((kSmemLimit - 1024) / stage);
+    const size_t stage = (size_t)(c.a_rows + F::bn) * kRowBytes;
+    c.stages = (int)((F::smem - 1024) / stage);
     if (c.stages > kMaxStages) c.stages = kMaxStages;
-    // the product reads 128 rows of x from every stage, loaded or not
     size_t need = (size_t)c.stages * stage;
-    if (need < (size_t)(c.stages - 1) * c.a_rows * kRowBytes + BM * kRowBytes)
-        need = (size_t)(c.stages - 1) * c.a_rows * kRowBytes + BM * kRowBytes;
-    if (need < sums) need = sums;
-    if (need < kSmemLeast) need = kSmemLeast;
+    // the product reads 128 rows of x from every stage, loaded or not
+    const size_t reach = (size_t)(c.stages - 1) * c.a_rows * kRowBytes + BM * kRowBytes;
+    const size_t sums = S > 1 ? (size_t)BM * (F::bn + 4) * 4 : 0;
+    // never more CTAs on an SM than the form is sized for: the next one's wait for TMEM could
+    // hold up a cluster
+    const size_t least = (size_t)(F::ctas == 1 ? 120 : 78) * 1024;
+    for (const size_t n : {reach, sums, least})
+        if (need < n) need = n;
     c.smem = need + 1024;
     return c;
 }
 
-template <int BN>
-uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p, int64_t tiles, bool overlap,
+Shape choose(int64_t M, int64_t N, int nk, int sms) {
+    const int64_t m_tiles = (M + BM - 1) / BM;
+    if (M > 64 && m_tiles * ((N + Wide::bn - 1) / Wide::bn) >= kWideTiles) return shape_of<Wide>(M, 1);
+    const bool half = m_tiles * ((N + 127) / 128) * 8 < sms;
+    const int64_t tiles = m_tiles * (half ? (N + 63) / 64 : (N + 127) / 128);
+    int S = 1;
+    while (S < kMaxSplit && tiles * S * 2 <= 2 * sms && nk >= S * 4) S *= 2;
+    return half ? shape_of<Narrow64>(M, S) : shape_of<Narrow128>(M, S);
+}
+
+template <class F>
+uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p, int sms, bool overlap,
                   cudaStream_t stream) {
-    uno_status s = check_cuda(cudaFuncSetAttribute(linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kSmemLimit + 1024),
-                              "cudaFuncSetAttribute(fp8 linear)");
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel's attributes are set and checked
+    int dev = 0;
+    uno_status s = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
     if (s != UNO_OK) return s;
+    const uint64_t bit = dev >= 0 && dev < kDevices ? 1ull << dev : 0ull;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        s = check_cuda(cudaFuncSetAttribute(linear_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem),
+                       "cudaFuncSetAttribute(fp8 linear)");
+        cudaFuncAttributes a;
+        if (s == UNO_OK) s = check_cuda(cudaFuncGetAttributes(&a, linear_kernel<F>), "cudaFuncGetAttributes(fp8 linear)");
+        if (s != UNO_OK) return s;
+        // the kernel's register split waits for what the launch did not bring
+        if (a.numRegs < F::regs)
+            return set_error(UNO_ERR_CUDA, "fp8 linear was built with %d registers a thread, %d are needed", a.numRegs,
+                             F::regs);
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    // persistent, except where a cluster shares a tile
+    const int64_t most = (int64_t)sms * F::ctas;
+    const int64_t units = c.S > 1 || p.tiles < most ? p.tiles : most;
+    if (units * c.S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attrs[2];
-    cfg.blockDim = dim3(kThreads);
-    cfg.gridDim = dim3((unsigned)(tiles * c.S));
+    cfg.blockDim = dim3((unsigned)F::threads);
+    cfg.gridDim = dim3((unsigned)(units * c.S));
     cfg.dynamicSmemBytes = c.smem;
     cfg.stream = stream;
     cfg.attrs = attrs;
-    attrs[0].id = cudaLaunchAttributeClusterDimension;
-    attrs[0].val.clusterDim.x = (unsigned)c.S;
-    attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = overlap ? 2 : 1;
-    return check_cuda(cudaLaunchKernelEx(&cfg, linear_kernel<BN>, maps[0], maps[1], maps[2], maps[3], p),
+    if (c.S > 1) {
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = (unsigned)c.S;
+        attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    if (overlap) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    return check_cuda(cudaLaunchKernelEx(&cfg, linear_kernel<F>, maps[0], maps[1], maps[2], maps[3], p),
                       "launch(fp8 linear)");
 }
 
@@ -489,7 +794,9 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     p.stages = c.stages;
     p.a_rows = c.a_rows;
     const int64_t tiles = (int64_t)p.m_tiles * ((p.N + c.BN - 1) / c.BN);
-    if (tiles * c.S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
+    // (K blocks are counted over a CTA's tiles in 32 bits)
+    if (tiles * (p.nk8 + p.nk16) > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
+    p.tiles = (int)tiles;
     CUtensorMap maps[4];
     uno_status s = UNO_OK;
     if (d_in) {
@@ -503,8 +810,9 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     if (s != UNO_OK) return s;
     if (!d_in) maps[0] = maps[2], maps[1] = maps[3];  // (not read)
     if (!r) maps[2] = maps[0], maps[3] = maps[1];
-    return c.BN == 64 ? launch<64>(c, maps, p, tiles, overlap, stream)
-                      : launch<128>(c, maps, p, tiles, overlap, stream);
+    return c.BN == Wide::bn        ? launch<Wide>(c, maps, p, sms, overlap, stream)
+           : c.BN == Narrow128::bn ? launch<Narrow128>(c, maps, p, sms, overlap, stream)
+                                   : launch<Narrow64>(c, maps, p, sms, overlap, stream);
 }
 
 }  // namespace fp8lin

@@ -14,7 +14,7 @@
 // Roles of a CTA's warps: 0 loads K blocks by TMA into a ring of shared-memory stages; 1 and 2
 // issue tcgen05.mma for the even and the odd K blocks, each into accumulators of its own
 // (waiting, issuing and committing a K block takes a warp about as long as its product); 3
-// brings the factors into shared memory, eight K blocks ahead; the others, four for each
+// copies the factors into shared memory, eight K blocks ahead; the others, four for each
 // column group, one for each quarter of the 128 TMEM lanes, drain the accumulators.
 // What set this shape, measured on 128 x 256 tiles in clocks per K block (its product takes
 // 512): 1900 with a release at cluster scope on the way back to the products; 1530 with each
@@ -45,7 +45,7 @@ constexpr int kRoles = 4;            // warps before the draining ones
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;         // CTAs that share a tile's K blocks
 constexpr int kChunk = 8;            // K blocks whose factors are staged together
-constexpr int kFactorPitch = BM + 4; // floats of a K block's factors (writes on 32 banks)
+constexpr int kFactorPitch = BM + 4; // floats of a K block's row factors (writes on 32 banks)
 
 struct Params {
     int M, N;              // rows and columns of Y
@@ -169,6 +169,15 @@ __device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&r)[16]) {
         : "memory");
 }
 
+// four bytes from global to shared memory, asynchronously; and this thread's arrival at an
+// mbarrier once all it has copied so far is there
+__device__ __forceinline__ void copy_async4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -193,19 +202,18 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
     return v;
 }
 
-// wait for an mbarrier phase (bounded); gives up early once another role of this CTA has
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+// Wait for an mbarrier phase (bounded); gives up early once another role of this CTA has. On
+// giving up it sets the flag and returns false.
+__device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
     for (uint32_t i = 0; i < kWaitLimit; i += 256) {
         if (mbar_wait(bar, parity, 256)) return true;
         if (*gave_up) return false;
     }
+    *gave_up = 1;
     return false;
 }
-
-// Two phases at once: their first polls are in flight together
-__device__ __forceinline__ bool wait_phases(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* gave_up) {
-    const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
-    return (ra || wait_phase(a, pa, gave_up)) && (rb || wait_phase(b, pb, gave_up));
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    return mbar_try_wait(bar, parity) || wait_longer(bar, parity, gave_up);
 }
 
 // two columns of a row's float32 sums in a register pair
@@ -343,7 +351,7 @@ struct Form {
     // split's sum may not exceed the launch's total.
     static constexpr int regs = CTAS == 1 ? 96 : 80, role_regs = 32, drain_regs = CTAS == 1 ? 112 : 104;
     static_assert(32 * kRoles * role_regs + 32 * EW * drain_regs <= threads * regs, "register split");
-    static constexpr int factor_bytes = 2 * halves * kChunk * kFactorPitch * 4;
+    static constexpr int factor_bytes = 2 * kChunk * (kFactorPitch + halves) * 4;
     // dynamic shared memory: the SM's 227 KB (1 KB less for each CTA) without the static part
     static constexpr int smem = (CTAS == 1 ? 226 * 1024 : 112 * 1024) - factor_bytes - 512;
 };
@@ -360,7 +368,10 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[NB], tempty[NB], sfull[2], sempty[2],
         drain[2];
-    __shared__ float factors[2][F::halves][kChunk][kFactorPitch];
+    __shared__ struct {
+        float x[2][kChunk][kFactorPitch];  // row factors
+        float w[2][F::halves][kChunk];     // column factors
+    } scales;
     __shared__ uint32_t tmem_base;
     __shared__ int s_gave_up;
 
@@ -388,7 +399,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
             mbar_init(&tempty[b], EW);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&sfull[b], 1);
+            mbar_init(&sfull[b], 64);  // a lane's copies, and its stores
             mbar_init(&sempty[b], EW);
             mbar_init(&drain[b], 1);
         }
@@ -418,10 +429,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         for (int tile = tile0; tile < p.tiles && !*gave_up; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
             for (int kb = kb0; kb < kb1; ++kb, ++got) {
-                if (got >= ST && !wait_phase(&empty[s], ph, gave_up)) {
-                    *gave_up = 1;
-                    break;
-                }
+                if (got >= ST && !wait_phase(&empty[s], ph, gave_up)) break;
                 const bool low = kb >= p.nk8;
                 if (low && !waited) {  // T comes from the kernel before this one
                     asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;" ::: "memory");
@@ -457,12 +465,10 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         uint32_t b = odd, bph = 1, s = odd % ST, ph = (odd / ST) & 1u;
         uint32_t kl = nkl ? odd % nkl : 0;
         for (uint32_t i = odd; i < mine * nkl; i += 2) {
-            const bool ok = i < (uint32_t)NB ? wait_phase(&full[s], ph, gave_up)
-                                             : wait_phases(&full[s], ph, &tempty[b], bph, gave_up);
-            if (!ok) {
-                *gave_up = 1;
-                break;
-            }
+            // (the two first polls are in flight together)
+            const bool free = i < (uint32_t)NB || mbar_try_wait(&tempty[b], bph);
+            if (!wait_phase(&full[s], ph, gave_up)) break;
+            if (!free && !wait_longer(&tempty[b], bph, gave_up)) break;
             fence_after();
             if (one) {
                 const uint64_t da = da0 + (uint64_t)((s * a_bytes) >> 4), db = db0 + (uint64_t)((s * b_bytes) >> 4);
@@ -497,51 +503,46 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         }
         __syncwarp();
     } else {
-        // factors[..][half][k][row] of the next eight K blocks: a row's scales of eight K blocks
-        // are one 32-byte sector, read once for the tile
+        // The scales of the next eight K blocks, copied without passing through registers: a row's
+        // eight are one 32-byte sector. (Through registers, four loads a lane at a time, this warp
+        // held up everything: 700 clocks a K block.) For the adapter's K blocks the row's factor is
+        // its gate, the column's the adapter's scale.
         uint32_t cb = 0, ph = 1, chunks = 0;
         bool ok = true;
         for (int tile = tile0; tile < p.tiles && ok; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
             for (int kc = kb0; kc < kb1; kc += kChunk, ++chunks) {
                 // this lane's K block kb = kc + lane % 8, rows lane / 8, + 4, + 8, ...
-                const int kb = kc + (lane & (kChunk - 1)), row = m0 + lane / kChunk;
+                const int k = lane & (kChunk - 1), kb = kc + k, row = m0 + lane / kChunk;
                 const bool low = kb >= p.nk8;
                 const float* src = low ? p.gate : p.xs;
                 const int step_row = low ? 1 : p.nk8;
                 if (src) src += low ? row : (int64_t)row * p.nk8 + kb;
-                float mul[F::halves];
-#pragma unroll
-                for (int h = 0; h < F::halves; ++h) {
-                    const int n = n0 + h * kBlockCols;
-                    mul[h] = kb >= kb1 || n >= p.N ? 0.f
-                             : !low                ? __ldg(p.ws + (int64_t)(n / kBlockCols) * p.nk8 + kb)
-                             : p.gate              ? p.scale
-                                                   : 1.f;
-                }
                 if (chunks >= 2) ok = wait_phase(&sempty[cb], ph, gave_up);
-                if (!ok) {
-                    *gave_up = 1;
-                    break;
+                if (!ok) break;
+                float* x = &scales.x[cb][k][lane / kChunk];
+                const int rows = kb < kb1 ? p.M - row : 0;
+                if (src) {
+#pragma unroll 8
+                    for (int r = 0; r < BM; r += 4)
+                        if (r < rows) copy_async4(x + r, src + (int64_t)r * step_row);
+                } else {
+                    for (int r = 0; r < BM; r += 4) x[r] = 1.f;
                 }
-                float* dst = &factors[cb][0][lane & (kChunk - 1)][lane / kChunk];
-#pragma unroll 1
-                for (int r = 0; r < BM && row + r < p.M; r += 16, dst += 16) {
-                    float x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[j] = row + r + 4 * j >= p.M ? 0.f : src ? __ldg(src + (int64_t)(r + 4 * j) * step_row) : 1.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int h = 0; h < F::halves; ++h) dst[h * kChunk * kFactorPitch + 4 * j] = x[j] * mul[h];
+                if (lane < F::halves * kChunk) {
+                    const int n = n0 + (lane / kChunk) * kBlockCols;
+                    float* w = &scales.w[cb][lane / kChunk][k];
+                    if (low) *w = p.gate ? p.scale : 1.f;
+                    else if (n < p.N && kb < kb1) copy_async4(w, p.ws + (int64_t)(n / kBlockCols) * p.nk8 + kb);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfull[cb]);
+                arrive_after_copies(&sfull[cb]);
+                mbar_arrive(&sfull[cb]);
                 cb ^= 1u;
                 if (cb == 0) ph ^= 1u;
             }
+            __syncwarp();
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
     }
     } else {
@@ -550,66 +551,74 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         // read ahead of those being added up, across K blocks too. ----
         const int quarter = warp & 3, group = (warp - kRoles) >> 2, r0 = quarter * 32;
         const uint32_t taddr = tmem + (uint32_t)(group * CW) + ((uint32_t)r0 << 16);
+        const int half = F::halves > 1 ? group * CW / kBlockCols : 0;
         uint32_t b = 0, bph = 0, cb = 0, sph = 0;
-        bool ok = true;
         uint64_t acc[CW / 2];  // (column pairs of one row)
-        for (int tile = tile0; tile < p.tiles && ok; tile += step) {
+        // A wait that gives up sets the flag, and the loops run on to their end: what they add up
+        // then is not stored.
+        auto next_block = [&](int k) {  // accumulator and factor of the CTA's K block k after this one
+            if (lane == 0) arrive_relaxed(&tempty[b]);
+            if (++b == (uint32_t)NB) {
+                b = 0;
+                bph ^= 1u;
+            }
+            if ((k & (kChunk - 1)) == 0 || kb0 + k == kb1) {  // the chunk of factors is used up
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sempty[cb]);
+                cb ^= 1u;
+                if (cb == 0) sph ^= 1u;
+            }
+        };
+        for (int tile = tile0; tile < p.tiles; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, col = (tile / p.m_tiles) * BN + group * CW;
-            const bool any = m0 + r0 < p.M;  // (a warp of rows past M only keeps the barriers going)
-            const float* fs = &factors[cb][F::halves > 1 ? group * CW / kBlockCols : 0][0][r0 + lane];
+            if (m0 + r0 >= p.M) {  // a warp of rows past M only keeps the barriers going
+                for (int k = 0; k < kb1 - kb0; ++k) {
+                    if ((k & (kChunk - 1)) == 0) wait_phase(&sfull[cb], sph, gave_up);
+                    wait_phase(&tfull[b], bph, gave_up);
+                    next_block(k + 1);
+                }
+                continue;
+            }
 #pragma unroll
             for (int j = 0; j < CW / 2; ++j) acc[j] = 0;
             float r[2][C];
-            ok = __all_sync(kFullMask, wait_phase(&sfull[cb], sph, gave_up) && wait_phase(&tfull[b], bph, gave_up));
-            if (!ok) {
-                *gave_up = 1;
-                break;
-            }
-            float f = *fs;
+            wait_phase(&sfull[cb], sph, gave_up);
+            float f = scales.x[cb][0][r0 + lane] * scales.w[cb][half][0];
+            wait_phase(&tfull[b], bph, gave_up);
             fence_after();
-            if (any) tmem_load(taddr + b * BN, r[0]);
-            for (int kb = kb0; kb < kb1; ++kb) {
+            __syncwarp();
+            tmem_load(taddr + b * BN, r[0]);
+            for (int k = 0; k < kb1 - kb0; ++k) {
                 const float fk = f;
-                const bool off = kb >= p.nk8 && fk == 0.f;  // no adapter on this row, whatever its product holds
 #pragma unroll
                 for (int c = 0; c < CW; c += C) {
-                    if (any) tmem_wait(r[c / C & 1]);
+                    tmem_wait(r[c / C & 1]);
                     if (c + C < CW) {
-                        if (any) tmem_load(taddr + b * BN + (uint32_t)(c + C), r[c / C + 1 & 1]);
+                        tmem_load(taddr + b * BN + (uint32_t)(c + C), r[c / C + 1 & 1]);
                     } else {
                         // this accumulator is read and may be filled again; on to the next one
                         fence_before();
-                        if (lane == 0) arrive_relaxed(&tempty[b]);
-                        if (++b == (uint32_t)NB) {
-                            b = 0;
-                            bph ^= 1u;
-                        }
-                        const int k = (kb + 1 - kb0) & (kChunk - 1);
-                        if (k == 0 || kb + 1 == kb1) {  // the chunk of factors is used up
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sempty[cb]);
-                            cb ^= 1u;
-                            if (cb == 0) sph ^= 1u;
-                            fs = &factors[cb][F::halves > 1 ? group * CW / kBlockCols : 0][0][r0 + lane];
-                        }
-                        if (kb + 1 < kb1) {
-                            bool there = wait_phase(&tfull[b], bph, gave_up);
-                            if (k == 0) there = there && wait_phase(&sfull[cb], sph, gave_up);
-                            ok = __all_sync(kFullMask, there);
-                            f = fs[k * kFactorPitch];
+                        next_block(k + 1);
+                        if (kb0 + k + 1 < kb1) {
+                            if (((k + 1) & (kChunk - 1)) == 0) wait_phase(&sfull[cb], sph, gave_up);
+                            const int kn = (k + 1) & (kChunk - 1);
+                            const float xs = scales.x[cb][kn][r0 + lane], ws = scales.w[cb][half][kn];
+                            wait_phase(&tfull[b], bph, gave_up);
+                            f = xs * ws;
                             fence_after();
-                            if (any && ok) tmem_load(taddr + b * BN, r[c / C + 1 & 1]);
+                            __syncwarp();
+                            tmem_load(taddr + b * BN, r[c / C + 1 & 1]);
                         }
                     }
-                    if (any && !off) add_scaled(acc, c, fk, r[c / C & 1]);
-                    __syncwarp();
-                }
-                if (!ok) {
-                    *gave_up = 1;
-                    break;
+                    if (kb0 + k < p.nk8) {
+                        add_scaled(acc, c, fk, r[c / C & 1]);
+                    } else {
+                        if (fk != 0.f) add_scaled(acc, c, fk, r[c / C & 1]);  // no adapter on a row whose factor is 0
+                        __syncwarp();
+                    }
                 }
             }
-            if (S == 1 && any && ok) store_rows<CW>(p, m0 + r0, col, lane, acc);
+            if (S == 1 && *gave_up == 0) store_rows<CW>(p, m0 + r0, col, lane, acc);
         }
         if (S > 1) {
             // ---- the CTAs' sums through shared memory (the ring: this CTA's products, which this
@@ -627,7 +636,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
             cluster_sync();
             // rank r of the cluster writes its share of the rows, four columns a thread
             const int first = (int)(rows * rank / S), n = ((int)(rows * (rank + 1) / S) - first) * (BN / 4);
-            for (int i = threadIdx.x - 32 * kRoles; i < n && ok; i += 32 * EW) {
+            for (int i = threadIdx.x - 32 * kRoles; i < n && *gave_up == 0; i += 32 * EW) {
                 const int r = first + i / (BN / 4), c = (i % (BN / 4)) * 4;
                 if (n0 + c >= p.N) continue;
                 const uint32_t at = ring + (uint32_t)(r * PITCH + c) * 4u;

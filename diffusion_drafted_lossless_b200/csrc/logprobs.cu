@@ -1,22 +1,22 @@
 // logprobs.cu — log probabilities of given tokens, entropy, the most probable alternatives,
 // and the gradient.
 //
-//   z = (x - ref) / T,  s = sum exp(z),  a = sum exp(z) z   (ref: near the row's maximum)
-//   log p_v = (x_v - max) / T - log s_max,   entropy = log s_max - a_max / s_max
+//   s = sum exp((x - ref) / T),  a = sum exp((x - ref) / T) (x - ref)    (ref: near the maximum)
+//   log p_v = (x_v - max) / T - log s_max,   entropy = log s_max - a_max / (s_max T)
 // where s_max, a_max are the sums moved to ref = max. exp is ex2 of (x - ref) (log2 e / T);
 // x - ref is taken before the product, so values of any size keep their differences.
 //
-// One pass over the row (bound: HBM). A row goes to a cluster of S CTAs, each with a run of
-// it; a thread streams 16-byte pieces, kUnroll of them in flight. The first pieces of all
-// threads are a sample: its maximum is every thread's first reference, so that references
-// move (and sums are rescaled) only where a value lies 64 octaves above; and the top_n-th
-// largest of the sample's 64 group maxima is a value that at least top_n tokens reach, so
-// only elements at or above it (a few hundred of a row) are candidates for the alternatives.
-// They are appended to a list in shared memory, and ranked at the end by counting, for each,
-// the candidates above it, value first and id second. A list that overflows (a row in
-// ascending order, a row of equal values) is no loss: its entries are real tokens, so the
-// top_n-th best of them bounds the search and the run is read again for what beats it, until
-// the list holds everything.
+// One pass over the row (bound: HBM, then the exponential unit: one ex2 an element). A row goes
+// to a cluster of S CTAs, each with a run of it; a thread streams 16-byte pieces, four added up
+// while the next four travel. The first eight pieces of all threads are a sample: its maximum is
+// every thread's first reference, so that references move (and sums are rescaled) only where a
+// value lies 64 octaves above; and the top_n-th largest of the sample's 64 group maxima is a
+// value that at least top_n tokens reach, so only elements at or above it (a few hundred of a
+// row) are candidates for the alternatives; after a quarter of a long run the candidates so far
+// raise that bound. They are appended to a list in shared memory and ranked at the end by
+// counting, value first and id second: a long list first in shares, one for each warp. A list that overflows (a row in ascending order, a row of equal values) is
+// no loss: its entries are real tokens, so the top_n-th best of them bounds the search and the
+// run is read again for what beats it, until the list holds everything.
 #include <cmath>
 #include <type_traits>
 
@@ -25,10 +25,11 @@
 namespace uno {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kUnroll = 4;
-constexpr int kGroups = 64;     // groups of 8 lanes whose maxima bound the search
+constexpr int kGroups = 64;     // groups of 4 lanes whose maxima bound the search
 constexpr int kList = 2048;     // candidates held; the second half keeps the latest ones
+constexpr int kQuick = 96;      // lists up to this long are ranked at once
 constexpr int kMaxTop = 32;
 constexpr int kMaxSplit = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -72,6 +73,9 @@ __device__ __forceinline__ float load_one(const T* p) {
     else return bf16_lo(__ldg(reinterpret_cast<const unsigned short*>(p)));
 }
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 // the largest of a piece (NaN passed over)
 template <typename T>
 __device__ __forceinline__ float piece_max(const uint4& v) {
@@ -85,27 +89,108 @@ __device__ __forceinline__ float piece_max(const uint4& v) {
     }
 }
 
-// A thread's running sums over what it has read: relative to ref, in octaves (z = arg ln 2)
-struct Sums {
-    float ref, max, s, a;
-};
-
-// the sums moved to another reference (delta = (old - new) c, at most 0 or with s = 0)
-__device__ __forceinline__ void move_ref(Sums& t, float to, float c) {
-    if (t.s > 0.f) {
-        const float d = (t.ref - to) * c, f = ex2(d);
-        t.a = f * fmaf(d, t.s, t.a);
-        t.s *= f;
-        if (f == 0.f) t.a = 0.f;
+// the largest of N pieces (NaN passed over)
+template <typename T, int N>
+__device__ __forceinline__ float pieces_max(const uint4 (&v)[N]) {
+    float m;
+    if constexpr (std::is_same_v<T, float>) {
+        m = piece_max<T>(v[0]);
+#pragma unroll
+        for (int u = 1; u < N; ++u) m = fmaxf(m, piece_max<T>(v[u]));
+    } else {
+        auto h = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+        __nv_bfloat162 m2 = __hmax2(__hmax2(h(v[0].x), h(v[0].y)), __hmax2(h(v[0].z), h(v[0].w)));
+#pragma unroll
+        for (int u = 1; u < N; ++u)
+            m2 = __hmax2(m2, __hmax2(__hmax2(h(v[u].x), h(v[u].y)), __hmax2(h(v[u].z), h(v[u].w))));
+        m = fmaxf(__low2float(m2), __high2float(m2));
     }
-    t.ref = to;
+    return fmaxf(m, -INFINITY);
+}
+
+// A thread's running sums over what it has read, in octaves: s = sum 2^arg, a = sum 2^arg arg.
+// Beside an ordinary reference (below 1e30 in size, the temperature below 1e20) arg is x c - R in
+// one rounding, R = ref c, and values below -1e30, -inf among them, count as -1e30: no weight
+// either way, and nothing overflows. Beside any other reference arg is (x - ref) c, and the two
+// kinds of sums never meet: the weights of one vanish beside the other's.
+struct Sums {
+    float ref, R, max, s, a;
+    bool ordinary;
+};
+constexpr float kLow = -1e30f;
+
+__device__ __forceinline__ void set_ref(Sums& t, float ref, float c, bool plain) {
+    t.ref = ref;
+    t.R = ref * c;
+    t.ordinary = plain && fabsf(ref) < 1e30f;
+}
+
+// the sums times 2^d, for a reference d octaves further up
+__device__ __forceinline__ void shift(Sums& t, float d) {
+    const float f = ex2(d);
+    t.a = f == 0.f ? 0.f : f * fmaf(d, t.s, t.a);
+    t.s *= f;
+}
+
+// move to another reference
+__device__ __forceinline__ void move_ref(Sums& t, float to, float c, bool plain) {
+    const Sums old = t;
+    set_ref(t, to, c, plain);
+    if (old.s == 0.f) t.a = 0.f;
+    else if (old.ordinary != t.ordinary) t.s = t.a = 0.f;
+    else shift(t, t.ordinary ? old.R - t.R : (old.ref - to) * c);
 }
 
 __device__ __forceinline__ void add_one(Sums& t, float x, float c) {
-    const float arg = exponent((x - t.ref) * c);  // (ref is finite or +inf: -inf has no weight)
-    const float e = ex2(arg);
+    // (an ordinary R is finite, any other ref is finite or +inf: -inf has no weight)
+    const float arg = exponent(t.ordinary ? fmaf(x, c, -t.R) : (x - t.ref) * c), e = ex2(arg);
     t.s += e;
     t.a = fmaf(e, arg, t.a);
+}
+
+// The pieces of a row beside an ordinary reference, two elements at a time.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ float2 two(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ void add_piece(const uint4& v, uint64_t minus_R, uint64_t c2, uint64_t& s2, uint64_t& a2) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr int N = 16 / (int)sizeof(T) / 2;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint64_t x;
+        if constexpr (std::is_same_v<T, float>) {
+            float lo, hi;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(__uint_as_float(w[2 * i])), "f"(kLow));
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(__uint_as_float(w[2 * i + 1])), "f"(kLow));
+            x = pair_of(lo, hi);
+        } else {
+            uint32_t m;
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w[i]), "r"(0xF14AF14Au));  // -1.0002e30 twice
+            x = pair_of(bf16_lo(m), bf16_hi(m));
+        }
+        const uint64_t arg = fma2(x, c2, minus_R);
+        const uint64_t e = pair_of(ex2(two(arg).x), ex2(two(arg).y));
+        s2 = add2(s2, e);
+        a2 = fma2(e, arg, a2);
+    }
 }
 
 // candidates found so far by this CTA, and the bound that new ones have to reach
@@ -123,6 +208,7 @@ __device__ __forceinline__ void append(const Search& q, float x, uint32_t id) {
 struct Args {
     int64_t V;
     float c, inv_t;            // log2 e / T, 1 / T
+    bool plain;                // values of -1e30 have no weight beside ordinary ones
     const int32_t* tokens;
     int top_n;
     float *logprob, *entropy, *stats;
@@ -160,11 +246,13 @@ __device__ __forceinline__ unsigned long long ld_peer_u64(const unsigned long lo
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* __restrict__ logits, const Args p) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restrict__ logits, const Args p) {
     constexpr int VE = kVec<T>;
     __shared__ unsigned long long list[kList];
     __shared__ unsigned long long best[kMaxTop];          // this run's top candidates, in order
-    __shared__ unsigned long long merged[kMaxSplit * kMaxTop];
+    __shared__ unsigned long long merged[kWarps * kMaxTop];  // the warps' or the CTAs' best
+    static_assert(kWarps >= kMaxSplit, "one array for both");
+    __shared__ uint4 laid[kWarps][32 * kUnroll];           // pieces that hold candidates
     __shared__ float group[kGroups];
     __shared__ float part[kWarps][4];
     __shared__ float run[4];                               // this run's ref, max, s, a
@@ -209,97 +297,143 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* __restri
 
     const Search q{list, &s_count};
     const float ninf = -INFINITY;
-    uint4 v[kUnroll];
     const uint32_t none = std::is_same_v<T, float> ? 0xFF800000u : 0xFF80FF80u;  // -inf
-    auto load = [&](int64_t i0) {
+    // turn `it` of this thread: pieces it * kTurn + tid, + kThreads, ... of the run
+    constexpr int kTurn = kUnroll * kThreads;
+    const int run_pieces = (int)(hi - lo), turns = (run_pieces + kTurn - 1) / kTurn;
+    const uint4* mine = body + lo + tid;
+    auto load = [&](uint4(&v)[kUnroll], int it) {
+        const uint4* at = mine + (int64_t)it * kTurn;
+        if ((it + 1) * (int64_t)kTurn <= run_pieces) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t i = i0 + (int64_t)u * kThreads;
-            v[u] = i < hi ? ld_stream_v4(body + i) : make_uint4(none, none, none, none);
+            for (int u = 0; u < kUnroll; ++u) v[u] = ld_stream_v4(at + u * kThreads);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                v[u] = it * (int64_t)kTurn + u * kThreads + tid < run_pieces ? ld_stream_v4(at + u * kThreads)
+                                                                            : make_uint4(none, none, none, none);
         }
     };
 
-    // ---- the sample: every thread's first pieces ----
-    load(lo + tid);
-    float m = ninf;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) m = fmaxf(m, piece_max<T>(v[u]));
+    // ---- the sample: every thread's first eight pieces ----
+    uint4 v0[kUnroll], v1[kUnroll];
+    load(v0, 0);
+    load(v1, 1);
+    const float m = fmaxf(pieces_max<T>(v0), pieces_max<T>(v1));
     float g = m;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(kFullMask, g, o));
-    if ((lane & 7) == 0) group[tid >> 3] = g;
-    if (tid == 0) s_count = 0;
+    for (int o = 2; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(kFullMask, g, o));
+    if ((lane & 3) == 0) group[tid >> 2] = g;
+    if (tid == 0) {
+        s_count = 0;
+        s_bound = ninf;
+    }
     __syncthreads();
-    if (warp == 0) {
-        const float g0 = group[lane], g1 = group[lane + 32];
-        if (lane == 0) s_bound = ninf;
-        const float top = warp_max(fmaxf(g0, g1));
-        if (k > 0) {
-            // ranks among the group maxima (equal ones by position): the k-th bounds the search
-            int r0 = 0, r1 = 0;
-            for (int j = 0; j < kGroups; ++j) {
-                const float o = group[j];
-                r0 += o > g0 || (o == g0 && j < lane);
-                r1 += o > g1 || (o == g1 && j < lane + 32);
-            }
-            __syncwarp();
-            if (r0 == k - 1) s_bound = g0;
-            if (r1 == k - 1) s_bound = g1;
+    {
+        // four threads rank a group's maximum among all (equal ones by position): the k-th bounds
+        // the search
+        const int mine = tid >> 2;
+        const float x = group[mine];
+        int r = 0;
+#pragma unroll
+        for (int j = 0; j < kGroups / 4; ++j) {
+            const int o = (tid & 3) * (kGroups / 4) + j;
+            const float y = group[o];
+            r += y > x || (y == x && o < mine);
         }
-        if (lane == 0) s_ref = fmaxf(top, -3.402823466e38f);  // finite where the sample is all -inf
+        r += __shfl_xor_sync(kFullMask, r, 1);
+        r += __shfl_xor_sync(kFullMask, r, 2);
+        if ((tid & 3) == 0) {
+            if (r == k - 1) s_bound = x;
+            if (r == 0) s_ref = fmaxf(x, -3.402823466e38f);  // finite where the sample is all -inf
+        }
     }
     __syncthreads();
 
-    Sums t{s_ref, ninf, 0.f, 0.f};
     const float c = p.c;
-    const float bound = s_bound;
-    // (the id of body element 0; ids are below 2^31)
-    const uint32_t id0 = (uint32_t)head;
-
-    auto candidates = [&](const uint4& w, int64_t i) {
-        float f[VE];
-        unpack<T>(w, f);
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-            if (f[e] >= bound && f[e] > ninf) append(q, f[e], id0 + (uint32_t)(i * VE + e));
-    };
+    Sums t;
+    set_ref(t, s_ref, c, p.plain);
+    t.max = ninf;
+    t.s = t.a = 0.f;
+    float bound = k > 0 ? s_bound : INFINITY;
+    // (the id of the run's first element; ids are below 2^31)
+    const uint32_t id0 = (uint32_t)(head + lo * VE);
 
     if (edge >= 0) {
         const float x = edge_x;
-        if (!((x - t.ref) * c <= 64.f)) move_ref(t, fmaxf(x, t.ref), c);
+        if (!((x - t.ref) * c <= 64.f)) move_ref(t, fmaxf(x, t.ref), c, p.plain);
         t.max = fmaxf(t.max, x);
         add_one(t, x, c);
-        if (k > 0 && x >= bound && x > ninf) append(q, x, (uint32_t)edge);
+        if (x >= bound && x > ninf) append(q, x, (uint32_t)edge);
     }
-    for (int64_t i0 = lo + tid; i0 < hi;) {
-        float pm[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) pm[u] = piece_max<T>(v[u]);
-        float cm = ninf;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) cm = fmaxf(cm, pm[u]);
+    auto take = [&](const uint4(&v)[kUnroll], int it) {
+        const float cm = pieces_max<T>(v);
         t.max = fmaxf(t.max, cm);
-        if ((cm - t.ref) * c > 64.f) move_ref(t, cm, c);
-        if (k > 0 && cm >= bound) {
+        if ((cm - t.ref) * c > 64.f) move_ref(t, cm, c, p.plain);
+        // lanes that hold a candidate lay their pieces down, and the warp looks at them together,
+        // one element a lane
+        unsigned hits = __ballot_sync(kFullMask, cm >= bound);
+        if (hits) {
+            if (cm >= bound) {
+                uint4* at = &laid[warp][__popc(hits & ((1u << lane) - 1u)) * kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (pm[u] >= bound) candidates(v[u], i0 + (int64_t)u * kThreads);
+                for (int u = 0; u < kUnroll; ++u) at[u] = v[u];
+            }
+            __syncwarp();
+            const T* at = reinterpret_cast<const T*>(&laid[warp][0]) + lane;
+            // this lane's element: of piece lane / VE, its lane % VE-th
+            const uint32_t id = id0 + (uint32_t)(it * kTurn + lane / VE * kThreads + warp * 32) * VE + lane % VE;
+            for (; hits; hits &= hits - 1, at += kUnroll * VE) {
+                if (lane < kUnroll * VE) {
+                    const float x = to_float(*at);
+                    if (x >= bound && x > ninf) append(q, x, id + (__ffs(hits) - 1) * VE);
+                }
+            }
+            __syncwarp();
         }
+        if (t.ordinary) {
+            const uint64_t minus_R = pair_of(-t.R, -t.R), c2 = pair_of(c, c);
+            uint64_t s2 = pair_of(t.s, 0.f), a2 = pair_of(t.a, 0.f);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float f[VE];
-            unpack<T>(v[u], f);
+            for (int u = 0; u < kUnroll; ++u) add_piece<T>(v[u], minus_R, c2, s2, a2);
+            t.s = two(s2).x + two(s2).y;
+            t.a = two(a2).x + two(a2).y;
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < kUnroll; ++u) {
+                float f[VE];
+                unpack<T>(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3], f);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) add_one(t, f[e], c);
+                for (int e = 0; e < VE; ++e) add_one(t, f[e], c);
+            }
         }
-        i0 += (int64_t)kUnroll * kThreads;
-        if (i0 < hi) load(i0);
+    };
+    // a quarter of a long run bounds the search more closely than the sample did
+    const int rebound = k > 0 && turns >= 8 ? turns / 4 & ~1 : -1;
+    for (int it = 0; it < turns; it += 2) {
+        if (it == rebound) {
+            __syncthreads();
+            const int held = (int)s_count;  // (above kThreads: too many for a quick look)
+            if (held <= kThreads && tid < held) {
+                const unsigned long long mine = list[tid];
+                int r = 0;
+                for (int o = 0; o < held; ++o) r += list[o] > mine;
+                if (r == k - 1) s_bound = key_float(candidate_key(mine));
+            }
+            __syncthreads();
+            bound = s_bound;
+        }
+        take(v0, it);
+        load(v0, it + 2);
+        if (it + 1 < turns) take(v1, it + 1);
+        load(v1, it + 3);
     }
 
     // ---- this run's sums, relative to its maximum ----
     auto combine = [&](float mx) {  // the block's sums at reference mx, valid in warp 0
-        if (t.s == 0.f) t.a = 0.f;
-        move_ref(t, mx, c);
+        const bool ordinary = p.plain && fabsf(mx) < 1e30f;
+        if (t.s == 0.f || t.ordinary != ordinary) t.s = t.s == t.s ? 0.f : t.s, t.a = 0.f;
+        else shift(t, ordinary ? fmaf(-mx, c, t.R) : (t.ref - mx) * c);
         const float s = warp_sum(t.s), a = warp_sum(t.a);
         if (lane == 0) part[warp][1] = s, part[warp][2] = a;
     };
@@ -317,26 +451,54 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* __restri
 
     // ---- this run's best k ----
     if (k > 0) {
-        unsigned long long kth = 0;  // candidates have to beat it (0: all do)
         for (;;) {
             const unsigned int found = s_count;
-            const unsigned int held = found < kList ? found : kList;
-            // rank of each held candidate (all differ: ids do)
-            for (unsigned int j = tid; j < held; j += kThreads) {
+            const int held = (int)(found < kList ? found : kList);
+            if (tid < k) best[tid] = 0;
+            if (held <= kQuick) {
+                __syncthreads();
+                if (tid < held) {
+                    const unsigned long long mine = list[tid];
+                    int r = 0;
+                    for (int o = 0; o < held; ++o) r += list[o] > mine;
+                    if (r < k) best[r] = mine;
+                }
+                __syncthreads();
+                break;
+            }
+            // each warp's share of the list (all entries differ: ids do), then the shares' best
+            const int from = held * warp / kWarps, to = held * (warp + 1) / kWarps;
+            merged[tid] = 0;
+            __syncwarp();  // (a warp's 32 places are its own)
+            for (int j = from + lane; j < to; j += 32) {
                 const unsigned long long mine = list[j];
                 int r = 0;
-                for (unsigned int o = 0; o < held && r < k; ++o) r += list[o] > mine;
+                for (int o = from; o < to && r < k; ++o) r += list[o] > mine;
+                if (r < k) merged[warp * kMaxTop + r] = mine;
+            }
+            __syncthreads();
+            const unsigned long long mine = merged[tid];
+            if (mine) {
+                // (each share's best are in order: how many of them are above, by bisection)
+                int r = 0;
+#pragma unroll 2
+                for (int w = 0; w < kWarps; ++w) {
+                    int n = 0;
+#pragma unroll
+                    for (int half = kMaxTop / 2; half > 0; half >>= 1)
+                        if (merged[w * kMaxTop + n + half - 1] > mine) n += half;
+                    r += n + (merged[w * kMaxTop + n] > mine);
+                }
                 if (r < k) best[r] = mine;
                 if (r == k - 1) s_kth = mine;
             }
             if (found <= kList) {
-                if (tid >= (int)held && tid < k) best[tid] = 0;
                 __syncthreads();
                 break;
             }
             // more were found than are held: read the run again for what beats the k-th held
             __syncthreads();
-            kth = s_kth;
+            const unsigned long long kth = s_kth;
             if (tid == 0) s_count = 0;
             __syncthreads();
             auto again = [&](float x, uint32_t id) {
@@ -348,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* __restri
                 float f[VE];
                 unpack<T>(w, f);
 #pragma unroll
-                for (int e = 0; e < VE; ++e) again(f[e], id0 + (uint32_t)(i * VE + e));
+                for (int e = 0; e < VE; ++e) again(f[e], (uint32_t)(head + i * VE + e));
             }
             __syncthreads();
         }
@@ -364,15 +526,15 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* __restri
             if (tid < (int)S * k) merged[tid] = ld_peer_u64(&best[tid % k], tid / k);
             if (warp == kWarps - 1) {
                 const bool in = lane < (int)S;
-                Sums r{ninf, ninf, 0.f, 0.f};
+                Sums r{};
+                r.max = ninf;
                 if (in) {
-                    r.ref = ld_peer_f32(&run[0], lane);
-                    r.max = r.ref;
+                    r.max = ld_peer_f32(&run[1], lane);
                     r.s = ld_peer_f32(&run[2], lane);
                     r.a = ld_peer_f32(&run[3], lane);
                 }
                 const float all = warp_max(r.max);
-                move_ref(r, all, c);
+                if (r.s != 0.f) shift(r, (r.max - all) * c);
                 const float s = warp_sum(r.s), a = warp_sum(r.a);
                 __syncwarp();
                 if (lane == 0) part[0][0] = all, part[0][1] = s, part[0][2] = a;
@@ -562,8 +724,8 @@ extern "C" uno_status uno_token_logprobs(const void* logits, uno_dtype dtype, in
     const void* ptrs[] = {logits, tokens, out_logprob, out_entropy, out_stats, out_top_ids, out_top_logprobs};
     for (const void* p : ptrs)
         if (off16(p)) return set_error(UNO_ERR_UNSUPPORTED, "tensor pointers must be 16-byte aligned");
-    const Args a{V, (float)(1.4426950408889634 / (double)temperature), 1.0f / temperature, tokens, top_n,
-                 out_logprob, out_entropy, out_stats, out_top_ids, out_top_logprobs};
+    const Args a{V, (float)(1.4426950408889634 / (double)temperature), 1.0f / temperature, temperature < 1e20f, tokens,
+                 top_n, out_logprob, out_entropy, out_stats, out_top_ids, out_top_logprobs};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return dtype == UNO_F32 ? logprobs_launch<float>(logits, N, a, st) : logprobs_launch<__nv_bfloat16>(logits, N, a, st);
 }

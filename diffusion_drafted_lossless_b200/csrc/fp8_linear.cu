@@ -344,7 +344,7 @@ template <int BN, int EW, int CTAS>
 struct Form {
     static constexpr int bn = BN, threads = 32 * (kRoles + EW), ctas = CTAS;
     static constexpr int CW = BN * 4 / EW;                     // columns of a draining warp
-    static constexpr int C = CTAS == 1 ? 16 : 8;               // columns read ahead (as registers allow)
+    static constexpr int C = CTAS == 1 || BN == 64 ? 16 : 8;   // columns read ahead (as registers allow)
     static constexpr int tmem = 512 / CTAS, NB = tmem / BN;
     static constexpr int halves = BN > kBlockCols ? BN / kBlockCols : 1;  // blocks of weight rows
     // registers a thread at launch, and after the split: the role warps give up theirs. The
@@ -389,6 +389,9 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     const int nk = p.nk8 + p.nk16;
     const int kb0 = (int)((int64_t)nk * rank / S), kb1 = (int)((int64_t)nk * (rank + 1) / S);
 
+    // draining warps that take part: with a single row tile, those whose rows exist (the others,
+    // polling barriers for nothing, took a third of the speed of a call of a few rows)
+    const int live = p.m_tiles == 1 ? EW / 4 * ((p.M + 31) / 32) : EW;
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < ST; ++s) {
             mbar_init(&full[s], 1);
@@ -396,11 +399,11 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         }
         for (int b = 0; b < NB; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], EW);
+            mbar_init(&tempty[b], live);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 64);  // a lane's copies, and its stores
-            mbar_init(&sempty[b], EW);
+            mbar_init(&sempty[b], live);
             mbar_init(&drain[b], 1);
         }
         s_gave_up = 0;
@@ -571,7 +574,8 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         };
         for (int tile = tile0; tile < p.tiles; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, col = (tile / p.m_tiles) * BN + group * CW;
-            if (m0 + r0 >= p.M) {  // a warp of rows past M only keeps the barriers going
+            if (p.m_tiles == 1 && r0 >= p.M) break;  // (not among the live ones)
+            if (m0 + r0 >= p.M) {  // rows past M in the last row tile: only keep the barriers going
                 for (int k = 0; k < kb1 - kb0; ++k) {
                     if ((k & (kChunk - 1)) == 0) wait_phase(&sfull[cb], sph, gave_up);
                     wait_phase(&tfull[b], bph, gave_up);
@@ -738,7 +742,7 @@ Shape shape_of(int64_t M, int S) {
 Shape choose(int64_t M, int64_t N, int nk, int sms) {
     const int64_t m_tiles = (M + BM - 1) / BM;
     if (M > 64 && m_tiles * ((N + Wide::bn - 1) / Wide::bn) >= kWideTiles) return shape_of<Wide>(M, 1);
-    const bool half = m_tiles * ((N + 127) / 128) * 8 < sms;
+    const bool half = m_tiles * ((N + 127) / 128) * 4 < sms;
     const int64_t tiles = m_tiles * (half ? (N + 63) / 64 : (N + 127) / 128);
     int S = 1;
     while (S < kMaxSplit && tiles * S * 2 <= 2 * sms && nk >= S * 4) S *= 2;

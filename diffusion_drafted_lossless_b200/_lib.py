@@ -9,6 +9,7 @@ fallback path, and a missing or unloadable libuno.so is an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from pathlib import Path
 
@@ -228,7 +229,7 @@ def uno_block_noise(clean_tokens, uniforms, V, noised_tokens, row_gate=None, str
 # include/uno_layers.h: every tensor's shape, dtype and device is checked here, and the call
 # runs on the tensors' device whichever one is current. The checks stand on the path of every
 # small call: they compare first and look for what to say only where a comparison fails.
-_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+_F8, _BF16, _F32, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
 _CODES = {torch.bfloat16: UNO_BF16, torch.float32: UNO_F32}
 
 
@@ -237,7 +238,7 @@ def _arg(name, t, shape, dtype, index):
     contiguous, of this shape and dtype, on CUDA device `index`."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape \
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
             and t.is_contiguous():
         return t.data_ptr()
     _ptr(t)
@@ -245,30 +246,43 @@ def _arg(name, t, shape, dtype, index):
                      f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _matrix(name, t, dtypes):
-    """Shape of a matrix of one of the dtypes, on a CUDA device."""
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+def _lead(name, t, dtypes):
+    """(shape, device address) of a contiguous CUDA matrix of one of the dtypes: an argument
+    whose shape the others are checked against."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous():
+        return t.shape, t.data_ptr()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _ptr(t)
-        raise ValueError(f"{name}: expected a matrix")
+        raise ValueError(f"{name}: a contiguous CUDA tensor is required")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix")
-    return t.shape
+    _ptr(t)
+    raise ValueError(f"{name}: expected a matrix, got {tuple(t.shape)}")
+
+
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# (torch's own accessor of the handle, without the Stream object, where this torch has it: a
+# microsecond of a small call)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _call(fn, index, stream, *args):
     """One library call on CUDA device `index`, enqueued on `stream` (default: that device's
     current one)."""
     if stream is None:
-        stream = torch.cuda.current_stream(index)
+        handle = _current_stream(index)
     elif stream.device_index != index:
         raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
+    else:
+        handle = stream.cuda_stream
     if index == torch.cuda.current_device():
-        status = fn(*args, stream.cuda_stream)
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, handle)
     if status != UNO_OK:
         _check(status)
 
@@ -281,9 +295,10 @@ def uno_rms_norm_fp8(x, weight, eps, out_q=None, out_scale=None, residual=None, 
                      stream=None):
     """RMS norm of x (+ residual) with e4m3 values and a scale per 128 columns, and / or the
     norm in x's dtype (see include/uno_layers.h)."""
-    shape = M, d = _matrix("x", x, _CODES)
+    shape, px = _lead("x", x, _CODES)
+    M, d = shape
     i, t = x.get_device(), x.dtype
-    _call(load().uno_rms_norm_fp8, i, stream, _arg("x", x, shape, t, i), _arg("residual", residual, shape, t, i),
+    _call(load().uno_rms_norm_fp8, i, stream, px, _arg("residual", residual, shape, t, i),
           _arg("weight", weight, (d,), t, i), _CODES[t], M, d, eps,
           _arg("out_residual", out_residual, shape, t, i), _arg("out_q", out_q, shape, _F8, i),
           _arg("out_scale", out_scale, (M, _blocks(d)), _F32, i), _arg("out_y", out_y, shape, t, i))
@@ -292,13 +307,14 @@ def uno_rms_norm_fp8(x, weight, eps, out_q=None, out_scale=None, residual=None, 
 def uno_fp8_quantize(x, out_q, out_scale, block_rows=1, stream=None):
     """e4m3 values and scales of x by block_rows x 128 blocks, block_rows 1 (activations) or
     128 (weights) (see include/uno_layers.h)."""
-    shape = M, d = _matrix("x", x, _CODES)
+    shape, px = _lead("x", x, _CODES)
+    M, d = shape
     i, t = x.get_device(), x.dtype
-    _call(load().uno_fp8_quantize, i, stream, _arg("x", x, shape, t, i), _CODES[t], M, d, block_rows,
-          _arg("out_q", out_q, shape, _F8, i),
+    _call(load().uno_fp8_quantize, i, stream, px, _CODES[t], M, d, block_rows, _arg("out_q", out_q, shape, _F8, i),
           _arg("out_scale", out_scale, (M if block_rows == 1 else _blocks(M), _blocks(d)), _F32, i))
 
 
+@functools.lru_cache(maxsize=1024)
 def uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank) -> int:
     return int(load().uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank))
 
@@ -307,26 +323,33 @@ def uno_fp8_gated_lora_linear(x_q, x_scale, w_q, w_scale, y, x=None, lora_a=None
                               scale=1.0, workspace=None, stream=None):
     """y = (x_q x_scale)(w_q w_scale)^T + scale * diag(row_gate) (x lora_a^T) lora_b^T, the
     adapter only where lora_a is given (see include/uno_layers.h)."""
-    M, d_in = x_shape = _matrix("x_q", x_q, (_F8,))
-    d_out = _matrix("w_q", w_q, (_F8,))[0]
-    _matrix("y", y, _CODES)
-    i, bf = x_q.get_device(), torch.bfloat16
-    rank = 0 if lora_a is None else _matrix("lora_a", lora_a, (bf,))[0]
-    ws, nb = None, 0
+    x_shape, px_q = _lead("x_q", x_q, (_F8,))
+    (d_out, w_in), pw_q = _lead("w_q", w_q, (_F8,))
+    y_shape, py = _lead("y", y, _CODES)
+    M, d_in = x_shape
+    i = x_q.get_device()
+    if w_in != d_in or y_shape != (M, d_out) or w_q.get_device() != i or y.get_device() != i:
+        raise ValueError(f"x_q {tuple(x_shape)}, w_q {(d_out, w_in)} and y {tuple(y_shape)} do not belong together "
+                         "or are on different devices")
+    rank, pa, pb, px, pg, ws, nb = 0, None, None, None, None, None, 0
+    if lora_a is not None:
+        (rank, _), _ = _lead("lora_a", lora_a, (_BF16,))
+        pa, pb = _arg("lora_a", lora_a, (rank, d_in), _BF16, i), _arg("lora_b", lora_b, (d_out, rank), _BF16, i)
+        px, pg = _arg("x", x, x_shape, _BF16, i), _arg("row_gate", row_gate, (M,), _F32, i)
     if rank:
-        made = workspace is None
-        ws, nb = _workspace(uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank), x_q.device, workspace)
-        if ws is not None and ws.get_device() != i:
-            raise ValueError(f"workspace is on {ws.device}, the tensors are on cuda:{i}")
-        if made and ws is not None and stream is not None:
-            ws.record_stream(stream)  # it may not be handed out again before this stream is done with it
-        ws = _ptr(ws)
-    _call(load().uno_fp8_gated_lora_linear, i, stream, _arg("x_q", x_q, x_shape, _F8, i),
-          _arg("x_scale", x_scale, (M, _blocks(d_in)), _F32, i), _arg("w_q", w_q, (d_out, d_in), _F8, i),
-          _arg("w_scale", w_scale, (_blocks(d_out), _blocks(d_in)), _F32, i), _arg("x", x, x_shape, bf, i),
-          _arg("lora_a", lora_a, (rank, d_in), bf, i), _arg("lora_b", lora_b, (d_out, rank), bf, i),
-          _arg("row_gate", row_gate, (M,), _F32, i), scale, M, d_in, d_out, rank,
-          _arg("y", y, (M, d_out), y.dtype, i), _CODES[y.dtype], ws, nb)
+        nb = uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank)
+        if workspace is None:
+            workspace = x_q.new_empty(nb, dtype=torch.uint8)
+            if stream is not None and nb:
+                workspace.record_stream(stream)  # not handed out again before this stream is done with it
+        elif workspace.get_device() != i:
+            raise ValueError(f"workspace is on {workspace.device}, the tensors are on cuda:{i}")
+        else:
+            nb = workspace.numel() * workspace.element_size()
+        ws = _ptr(workspace)
+    _call(load().uno_fp8_gated_lora_linear, i, stream, px_q, _arg("x_scale", x_scale, (M, _blocks(d_in)), _F32, i),
+          pw_q, _arg("w_scale", w_scale, (_blocks(d_out), _blocks(d_in)), _F32, i), px, pa, pb, pg, scale, M, d_in,
+          d_out, rank, py, _CODES[y.dtype], ws, nb)
     return y
 
 
@@ -335,25 +358,27 @@ def uno_token_logprobs(logits, tokens, out_logprob=None, temperature=1.0, out_en
     """Log probability of each row's token, entropy, the most probable tokens (as many as
     out_top_ids has columns), and the statistics the gradient needs; rows whose token is not
     in [0, V) are left out (see include/uno_layers.h)."""
-    shape = N, V = _matrix("logits", logits, _CODES)
+    (N, V), p = _lead("logits", logits, _CODES)
     i, t = logits.get_device(), logits.dtype
-    k = 0 if out_top_ids is None else _matrix("out_top_ids", out_top_ids, (_I32,))[1]
-    ids = lps = None
-    if k:
-        ids, lps = _arg("out_top_ids", out_top_ids, (N, k), _I32, i), \
-            _arg("out_top_logprobs", out_top_logprobs, (N, k), _F32, i)
-    _call(load().uno_token_logprobs, i, stream, _arg("logits", logits, shape, t, i), _CODES[t], N, V, temperature,
-          _arg("tokens", tokens, (N,), _I32, i), k, _arg("out_logprob", out_logprob, (N,), _F32, i),
-          _arg("out_entropy", out_entropy, (N,), _F32, i), _arg("out_stats", out_stats, (N, 2), _F32, i), ids, lps)
+    k, ids, lps = 0, None, None
+    if out_top_ids is not None or out_top_logprobs is not None:
+        (_, k), _ = _lead("out_top_ids", out_top_ids, (_I32,))
+        if k:
+            ids = _arg("out_top_ids", out_top_ids, (N, k), _I32, i)
+            lps = _arg("out_top_logprobs", out_top_logprobs, (N, k), _F32, i)
+    _call(load().uno_token_logprobs, i, stream, p, _CODES[t], N, V, temperature, _arg("tokens", tokens, (N,), _I32, i),
+          k, _arg("out_logprob", out_logprob, (N,), _F32, i), _arg("out_entropy", out_entropy, (N,), _F32, i),
+          _arg("out_stats", out_stats, (N, 2), _F32, i), ids, lps)
 
 
 def uno_token_logprobs_grad(logits, tokens, stats, grad_logits, grad_logprob=None, entropy=None, grad_entropy=None,
                             temperature=1.0, stream=None):
     """Gradient of uno_token_logprobs' log probabilities and entropies with respect to the
     logits; grad_logits may be logits itself (see include/uno_layers.h)."""
-    shape = N, V = _matrix("logits", logits, _CODES)
+    shape, p = _lead("logits", logits, _CODES)
+    N, V = shape
     i, t = logits.get_device(), logits.dtype
-    _call(load().uno_token_logprobs_grad, i, stream, _arg("logits", logits, shape, t, i), _CODES[t], N, V, temperature,
+    _call(load().uno_token_logprobs_grad, i, stream, p, _CODES[t], N, V, temperature,
           _arg("tokens", tokens, (N,), _I32, i), _arg("stats", stats, (N, 2), _F32, i),
           _arg("entropy", entropy, (N,), _F32, i), _arg("grad_logprob", grad_logprob, (N,), _F32, i),
           _arg("grad_entropy", grad_entropy, (N,), _F32, i), _arg("grad_logits", grad_logits, shape, t, i))

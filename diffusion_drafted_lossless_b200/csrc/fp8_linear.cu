@@ -50,8 +50,7 @@ constexpr int kFactorPitch = BM + 4; // floats of a K block's row factors (write
 struct Params {
     int M, N;              // rows and columns of Y
     int nk8, nk16;         // K blocks of e4m3 and of bf16
-    int m_tiles;           // row tiles
-    int first, tiles;      // this launch's tiles: first .. tiles - 1
+    int m_tiles, tiles;    // row tiles, all tiles
     int stages;
     uint32_t a_rows;       // rows of x loaded per K block (a multiple of 8, at most 128)
     const float* xs;       // [M, nk8]
@@ -61,7 +60,6 @@ struct Params {
     void* y;
     int y_f32;
     int wait_t;            // the bf16 blocks' x operand is the previous kernel's output
-    int join;              // end after the kernel before this one
     uint32_t* status;
 };
 
@@ -386,7 +384,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* gave_up = &s_gave_up;
     const uint32_t S = F::ctas == 1 ? 1u : cluster_size(), rank = F::ctas == 1 ? 0u : cluster_rank();
-    const int tile0 = p.first + blockIdx.x / S, step = gridDim.x / S;
+    const int tile0 = blockIdx.x / S, step = gridDim.x / S;
     // this CTA's share of the K blocks of its tiles
     const int nk = p.nk8 + p.nk16;
     const int kb0 = (int)((int64_t)nk * rank / S), kb1 = (int)((int64_t)nk * (rank + 1) / S);
@@ -672,8 +670,6 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::tmem) : "memory");
     if (threadIdx.x == 0 && *gave_up) record_device_status(p.status, (uint32_t)UNO_ERR_TIMEOUT);
-    // (this grid ran beside the one before it; what follows on the stream waits for this one only)
-    if (p.join) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------
@@ -774,8 +770,8 @@ uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p,
         ready.fetch_or(bit, std::memory_order_release);
     }
     // persistent, except where a cluster shares a tile
-    const int64_t most = (int64_t)sms * F::ctas, tiles = p.tiles - p.first;
-    const int64_t units = c.S > 1 || tiles < most ? tiles : most;
+    const int64_t most = (int64_t)sms * F::ctas;
+    const int64_t units = c.S > 1 || p.tiles < most ? p.tiles : most;
     if (units * c.S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attrs[2];
@@ -827,25 +823,9 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     if (s != UNO_OK) return s;
     if (!d_in) maps[0] = maps[2], maps[1] = maps[3];  // (not read)
     if (!r) maps[2] = maps[0], maps[3] = maps[1];
-    if (c.BN == Wide::bn) return launch<Wide>(c, maps, p, sms, overlap, stream);
-    if (c.BN == Narrow64::bn) return launch<Narrow64>(c, maps, p, sms, overlap, stream);
-    // Where the last turn of the persistent CTAs would leave half of them or more without a tile,
-    // its tiles are shared by clusters instead, in a launch that starts as the others finish: a
-    // head of 151936 columns over 64 rows (1187 tiles for 296 CTAs) takes 4 turns and a bit in
-    // place of 5.
-    const int64_t units = (int64_t)sms * Narrow128::ctas, rest = tiles % units;
-    int S = 1;
-    while (S < kMaxSplit && rest * S * 2 <= units && p.nk8 + p.nk16 >= S * 4) S *= 2;
-    if (c.S > 1 || tiles < units || rest == 0 || S == 1) return launch<Narrow128>(c, maps, p, sms, overlap, stream);
-    p.tiles = (int)(tiles - rest);
-    s = launch<Narrow128>(c, maps, p, sms, overlap, stream);
-    if (s != UNO_OK) return s;
-    p.first = p.tiles;
-    p.tiles = (int)tiles;
-    p.join = 1;
-    const Shape tail = shape_of<Narrow128>(p.M, S);
-    p.stages = tail.stages;
-    return launch<Narrow128>(tail, maps, p, sms, true, stream);
+    return c.BN == Wide::bn        ? launch<Wide>(c, maps, p, sms, overlap, stream)
+           : c.BN == Narrow128::bn ? launch<Narrow128>(c, maps, p, sms, overlap, stream)
+                                   : launch<Narrow64>(c, maps, p, sms, overlap, stream);
 }
 
 }  // namespace fp8lin

@@ -72,6 +72,19 @@ def test_large_products_on_sampled_rows():
         _check(part, y[rows.cuda()])
 
 
+@pytest.mark.parametrize("M,d_in,d_out,rank,dtype", [
+    (9, 640, 40001, 0, BF), (16, 1152, 39000, 0, F32), (24, 512, 40000, 64, BF), (33, 384, 39168, 16, BF),
+    (64, 768, 38400, 0, BF), (31, 256, 300, 8, BF), (32, 2048, 129, 0, F32), (17, 4096, 2056, 200, BF),
+    (8, 16, 128, 0, F32), (25, 144, 64, 0, BF),
+])
+def test_few_rows_and_last_turns(M, d_in, d_out, rank, dtype):
+    """Calls of at most 64 rows, and widths of more than two tiles of 128 columns an SM, a few
+    over: the last turn of the persistent CTAs is mostly empty."""
+    o = _operands(M, d_in, d_out, rank)
+    y = torch.full((M, d_out), math.nan, dtype=dtype, device="cuda")
+    _check(o, _run(_cuda(o), y))
+
+
 def test_rows_without_gate_are_the_base_product():
     o = _operands(70, 512, 384, 32)
     c = _cuda(o)
@@ -155,6 +168,21 @@ def test_two_streams_dirty_workspaces_and_graphs():
         torch.cuda.synchronize()
         for k in range(2):
             _check(o, ys[k])
+
+
+@pytest.mark.parametrize("M,d_in,d_out,rank", [(24, 512, 4000, 64), (16, 4096, 4096, 128), (40, 1024, 20000, 64),
+                                               (200, 512, 9728, 64), (700, 1024, 9728, 128)])
+def test_the_adapter_reads_what_this_call_made(M, d_in, d_out, rank):
+    """The projection starts beside the kernel that makes T and waits for it: with the workspace
+    overwritten between calls, every call gives the first one's bits."""
+    c = _cuda(_operands(M, d_in, d_out, rank))
+    ws = torch.empty(_lib.uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank), dtype=torch.uint8,
+                     device="cuda")
+    first = _run(c, torch.empty((M, d_out), dtype=BF, device="cuda"), workspace=ws)
+    y = torch.empty_like(first)
+    for _ in range(60):
+        ws.fill_(0x45)
+        assert torch.equal(_run(c, y, workspace=ws), first)
 
 
 def test_same_bits_every_time():

@@ -22,11 +22,10 @@
 // read their operands from); 1480 with TMEM reads, waits and additions in turn; ~1000 of them
 // for a barrier of all drains around the staging of scales.
 //
-// Two forms:
-//   wide (large products): 128 x 256 tiles, one CTA per SM, persistent, sixteen draining warps
-//   narrow: 128 x 128 or 128 x 64 tiles, two CTAs per SM, eight draining warps; a cluster of S
-//     CTAs shares a tile's K blocks where there are few tiles, and adds its sums up through
-//     distributed shared memory, in rank order
+// Forms (one CTA per SM in each):
+//   wide (large products): 128 x 256 tiles, persistent
+//   narrow: 128 x 128 or 128 x 64 tiles; a cluster of S CTAs shares a tile's K blocks where there
+//     are few tiles, and adds its sums up through distributed shared memory, in rank order
 // Rows past M are never stored; a small M shrinks the loaded rows of x, not the product.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -42,7 +41,7 @@ namespace fp8lin {
 constexpr int BM = 128;
 constexpr int kRowBytes = 128;       // bytes of a K block's row: one 128-byte swizzle row
 constexpr int kRoles = 4;            // warps before the draining ones
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 16;
 constexpr int kMaxSplit = 8;         // CTAs that share a tile's K blocks
 constexpr int kChunk = 8;            // K blocks whose factors are staged together
 constexpr int kFactorPitch = BM + 4; // floats of a K block's row factors (writes on 32 banks)
@@ -59,7 +58,6 @@ struct Params {
     float scale;
     void* y;
     int y_f32;
-    int wait_t;            // the bf16 blocks' x operand is the previous kernel's output
     uint32_t* status;
 };
 
@@ -191,6 +189,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void block_sync() { asm volatile("barrier.sync.aligned 0;" ::: "memory"); }
 __device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
     uint32_t remote;
     float4 v;
@@ -206,8 +205,8 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
 // giving up it sets the flag and returns false.
 __device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
     for (uint32_t i = 0; i < kWaitLimit; i += 256) {
-        if (mbar_wait(bar, parity, 256)) return true;
         if (*gave_up) return false;
+        if (mbar_wait(bar, parity, 256)) return true;
     }
     *gave_up = 1;
     return false;
@@ -337,30 +336,33 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, co
 }
 
 // ---------------------------------------------------------------------------------------
-// BN: columns of a tile; EW: draining warps; CTAS: CTAs per SM that registers, TMEM and shared
-// memory are sized for. NB accumulators of BN columns share the CTA's 512 / CTAS of TMEM.
+// BN: columns of a tile; EW: draining warps. One CTA per SM: that is all the runtime's occupancy
+// query allows this kernel, whatever its size. (Forms of half an SM, two of whose CTAs the
+// hardware did place on one, failed with "unspecified launch failure" once in some thousand
+// calls, on an SM that held two.) NB accumulators of BN columns share the SM's TMEM.
 // ---------------------------------------------------------------------------------------
-template <int BN, int EW, int CTAS>
+template <int BN, int EW>
 struct Form {
-    static constexpr int bn = BN, threads = 32 * (kRoles + EW), ctas = CTAS;
-    static constexpr int CW = BN * 4 / EW;                     // columns of a draining warp
-    static constexpr int C = CTAS == 1 || BN == 64 ? 16 : 8;   // columns read ahead (as registers allow)
-    static constexpr int tmem = 512 / CTAS, NB = tmem / BN;
+    static constexpr int bn = BN, threads = 32 * (kRoles + EW);
+    static constexpr int CW = BN * 4 / EW;          // columns of a draining warp
+    static constexpr int C = CW / 2 < 16 ? CW / 2 : 16;  // columns read ahead: CW / C is even
+    static constexpr int tmem = 512, NB = tmem / BN;
     static constexpr int halves = BN > kBlockCols ? BN / kBlockCols : 1;  // blocks of weight rows
     // registers a thread at launch, and after the split: the role warps give up theirs. The
     // split's sum may not exceed the launch's total.
-    static constexpr int regs = CTAS == 1 ? 96 : 80, role_regs = 32, drain_regs = CTAS == 1 ? 112 : 104;
-    static_assert(32 * kRoles * role_regs + 32 * EW * drain_regs <= threads * regs, "register split");
+    static constexpr bool split = CW > 32;
+    static constexpr int regs = 96, role_regs = 32, drain_regs = 112;
+    static_assert(!split || 32 * kRoles * role_regs + 32 * EW * drain_regs <= threads * regs, "register split");
     static constexpr int factor_bytes = 2 * kChunk * (kFactorPitch + halves) * 4;
-    // dynamic shared memory: the SM's 227 KB (1 KB less for each CTA) without the static part
-    static constexpr int smem = (CTAS == 1 ? 226 * 1024 : 112 * 1024) - factor_bytes - 512;
+    // dynamic shared memory: the SM's 227 KB without the static part
+    static constexpr int smem = 226 * 1024 - factor_bytes - 768;
 };
-using Wide = Form<256, 16, 1>;
-using Narrow128 = Form<128, 8, 2>;
-using Narrow64 = Form<64, 8, 2>;
+using Wide = Form<256, 16>;
+using Narrow128 = Form<128, 16>;
+using Narrow64 = Form<64, 16>;
 
 template <class F>
-__global__ void __launch_bounds__(F::threads, F::ctas)
+__global__ void __launch_bounds__(F::threads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CUtensorMap tW,
               const __grid_constant__ CUtensorMap tT, const __grid_constant__ CUtensorMap tB, const Params p) {
     constexpr int BN = F::bn, CW = F::CW, C = F::C, NB = F::NB, EW = F::threads / 32 - kRoles;
@@ -383,7 +385,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* gave_up = &s_gave_up;
-    const uint32_t S = F::ctas == 1 ? 1u : cluster_size(), rank = F::ctas == 1 ? 0u : cluster_rank();
+    const uint32_t S = F::bn == 256 ? 1u : cluster_size(), rank = F::bn == 256 ? 0u : cluster_rank();
     const int tile0 = blockIdx.x / S, step = gridDim.x / S;
     // this CTA's share of the K blocks of its tiles
     const int nk = p.nk8 + p.nk16;
@@ -419,26 +421,19 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
-    // the next kernel on the stream may start its own prologue (it waits for this grid's end
-    // before it reads what this one writes)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp < kRoles) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::role_regs));
+    if (F::split) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::role_regs));
     if (warp == 0) {
         const bool one = elect_one();
         uint32_t s = 0, ph = 1, got = 0;
-        bool waited = !p.wait_t;
-        for (int tile = tile0; tile < p.tiles && !*gave_up; tile += step) {
+        bool ok = true;  // (a lane that has given up keeps the others company)
+        for (int tile = tile0; tile < p.tiles; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
-            for (int kb = kb0; kb < kb1; ++kb, ++got) {
-                if (got >= ST && !wait_phase(&empty[s], ph, gave_up)) break;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = ok && (got < ST || wait_phase(&empty[s], ph, gave_up));
                 const bool low = kb >= p.nk8;
-                if (low && !waited) {  // T comes from the kernel before this one
-                    asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;" ::: "memory");
-                    waited = true;
-                }
-                if (one) {
+                if (one && ok) {
                     mbar_arrive_expect_tx(&full[s], a_bytes + b_bytes);
                     const uint32_t a = ring + s * a_bytes, b = ring_b + s * b_bytes;
                     if (low) {
@@ -449,15 +444,22 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                         load_2d(b, &tW, kb * 128, n0, &full[s]);
                     }
                 }
+                __syncwarp();  // (a lane left behind by two phases would wait for a third)
+                got += ok;
                 if (++s == ST) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
-            __syncwarp();
         }
-        if (*gave_up)  // loads that no product will read: let them land
-            for (uint32_t j = got > ST ? got - ST : 0; j < got; ++j) mbar_wait(&full[j % ST], (j / ST) & 1, 1u << 16);
+        // Nothing may still be on its way to this CTA's shared memory when it ends: the last commits
+        // arrive at `empty` on their own, after the accumulators they follow have been seen (an
+        // arrival at the barriers of the next CTA in this place would break its ring). Loads that
+        // no product will read: let them land.
+        for (uint32_t j = got > ST ? got - ST : 0; j < got; ++j) {
+            if (*gave_up) mbar_wait(&full[j % ST], (j / ST) & 1, 1u << 16);
+            else wait_phase(&empty[j % ST], (j / ST) & 1, gave_up);
+        }
         __syncwarp();
     } else if (warp <= 2) {
         // K block i of the CTA goes to accumulator i mod NB (NB is even)
@@ -467,13 +469,13 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         const uint32_t mine = p.tiles > tile0 ? (uint32_t)((p.tiles - 1 - tile0) / step + 1) : 0u;
         uint32_t b = odd, bph = 1, s = odd % ST, ph = (odd / ST) & 1u;
         uint32_t kl = nkl ? odd % nkl : 0;
+        bool ok = true;
         for (uint32_t i = odd; i < mine * nkl; i += 2) {
             // (the two first polls are in flight together)
             const bool free = i < (uint32_t)NB || mbar_try_wait(&tempty[b], bph);
-            if (!wait_phase(&full[s], ph, gave_up)) break;
-            if (!free && !wait_longer(&tempty[b], bph, gave_up)) break;
+            ok = ok && wait_phase(&full[s], ph, gave_up) && (free || wait_longer(&tempty[b], bph, gave_up));
             fence_after();
-            if (one) {
+            if (one && ok) {
                 const uint64_t da = da0 + (uint64_t)((s * a_bytes) >> 4), db = db0 + (uint64_t)((s * b_bytes) >> 4);
                 const uint32_t d = tmem + b * BN;
                 if (kb0 + (int)kl < p.nk8) {
@@ -487,6 +489,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                 commit(&tfull[b]);
                 commit(&empty[s]);
             }
+            __syncwarp();  // (a lane left behind by two phases would wait for a third)
             s += 2;
             if (s >= ST) {
                 s -= ST;
@@ -499,7 +502,6 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
             }
             for (kl += 2; kl >= nkl;) kl -= nkl;
         }
-        __syncwarp();
         if (*gave_up) {  // products in flight end before their memory is given back
             if (one) commit(&drain[odd]);
             mbar_wait(&drain[odd], 0, 1u << 16);
@@ -512,7 +514,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         // its gate, the column's the adapter's scale.
         uint32_t cb = 0, ph = 1, chunks = 0;
         bool ok = true;
-        for (int tile = tile0; tile < p.tiles && ok; tile += step) {
+        for (int tile = tile0; tile < p.tiles; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
             for (int kc = kb0; kc < kb1; kc += kChunk, ++chunks) {
                 // this lane's K block kb = kc + lane % 8, rows lane / 8, + 4, + 8, ...
@@ -521,25 +523,26 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                 const float* src = low ? p.gate : p.xs;
                 const int step_row = low ? 1 : p.nk8;
                 if (src) src += low ? row : (int64_t)row * p.nk8 + kb;
-                if (chunks >= 2) ok = wait_phase(&sempty[cb], ph, gave_up);
-                if (!ok) break;
-                float* x = &scales.x[cb][k][lane / kChunk];
-                const int rows = kb < kb1 ? p.M - row : 0;
-                if (src) {
+                ok = ok && (chunks < 2 || wait_phase(&sempty[cb], ph, gave_up));
+                if (ok) {
+                    float* x = &scales.x[cb][k][lane / kChunk];
+                    const int rows = kb < kb1 ? p.M - row : 0;
+                    if (src) {
 #pragma unroll 8
-                    for (int r = 0; r < BM; r += 4)
-                        if (r < rows) copy_async4(x + r, src + (int64_t)r * step_row);
-                } else {
-                    for (int r = 0; r < BM; r += 4) x[r] = 1.f;
+                        for (int r = 0; r < BM; r += 4)
+                            if (r < rows) copy_async4(x + r, src + (int64_t)r * step_row);
+                    } else {
+                        for (int r = 0; r < BM; r += 4) x[r] = 1.f;
+                    }
+                    if (lane < F::halves * kChunk) {
+                        const int n = n0 + (lane / kChunk) * kBlockCols;
+                        float* w = &scales.w[cb][lane / kChunk][k];
+                        if (low) *w = p.gate ? p.scale : 1.f;
+                        else if (n < p.N && kb < kb1) copy_async4(w, p.ws + (int64_t)(n / kBlockCols) * p.nk8 + kb);
+                    }
+                    arrive_after_copies(&sfull[cb]);
+                    mbar_arrive(&sfull[cb]);
                 }
-                if (lane < F::halves * kChunk) {
-                    const int n = n0 + (lane / kChunk) * kBlockCols;
-                    float* w = &scales.w[cb][lane / kChunk][k];
-                    if (low) *w = p.gate ? p.scale : 1.f;
-                    else if (n < p.N && kb < kb1) copy_async4(w, p.ws + (int64_t)(n / kBlockCols) * p.nk8 + kb);
-                }
-                arrive_after_copies(&sfull[cb]);
-                mbar_arrive(&sfull[cb]);
                 cb ^= 1u;
                 if (cb == 0) ph ^= 1u;
             }
@@ -548,8 +551,20 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
     }
+    // (each side of the register split runs to its end by itself: nothing behind a join is
+    // compiled for the larger share and run by a warp of the smaller)
+    if (S > 1) {
+        cluster_sync();  // (the sums are laid down)
+        cluster_sync();  // no CTA leaves while another reads its sums
+    }
+    fence_before();
+    block_sync();
+    fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::tmem) : "memory");
+    if (threadIdx.x == 0 && *gave_up) record_device_status(p.status, (uint32_t)UNO_ERR_TIMEOUT);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::drain_regs));
+        if (F::split) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::drain_regs));
         // ---- draining: acc += factor * accumulator, one row a thread, CW columns. C columns are
         // read ahead of those being added up, across K blocks too. ----
         const int quarter = warp & 3, group = (warp - kRoles) >> 2, r0 = quarter * 32;
@@ -579,6 +594,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                 for (int k = 0; k < kb1 - kb0; ++k) {
                     if ((k & (kChunk - 1)) == 0) wait_phase(&sfull[cb], sph, gave_up);
                     wait_phase(&tfull[b], bph, gave_up);
+                    __syncwarp();
                     next_block(k + 1);
                 }
                 continue;
@@ -654,22 +670,13 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                     v.x += part[k].x, v.y += part[k].y, v.z += part[k].z, v.w += part[k].w;
                 store4(p, m0 + r, n0 + c, v);
             }
+            __syncwarp();
+            cluster_sync();  // no CTA leaves while another reads its sums
         }
         __syncwarp();
+        fence_before();
+        block_sync();
     }
-
-    if (S > 1) {
-        __syncwarp();
-        if (warp < kRoles) cluster_sync();  // (the draining warps' turn is above)
-        __syncwarp();
-        cluster_sync();  // no CTA leaves while another reads its sums
-    }
-    fence_before();
-    __syncthreads();
-    fence_after();
-    if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(F::tmem) : "memory");
-    if (threadIdx.x == 0 && *gave_up) record_device_status(p.status, (uint32_t)UNO_ERR_TIMEOUT);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -730,65 +737,99 @@ Shape shape_of(int64_t M, int S) {
     // the product reads 128 rows of x from every stage, loaded or not
     const size_t reach = (size_t)(c.stages - 1) * c.a_rows * kRowBytes + BM * kRowBytes;
     const size_t sums = S > 1 ? (size_t)BM * (F::bn + 4) * 4 : 0;
-    // never more CTAs on an SM than the form is sized for: the next one's wait for TMEM could
-    // hold up a cluster
-    const size_t least = (size_t)(F::ctas == 1 ? 120 : 78) * 1024;
+    const size_t least = 120 * 1024;  // more than half an SM's: one CTA on each
     for (const size_t n : {reach, sums, least})
         if (need < n) need = n;
     c.smem = need + 1024;
     return c;
 }
 
-Shape choose(int64_t M, int64_t N, int nk, int sms) {
-    const int64_t m_tiles = (M + BM - 1) / BM;
-    if (M > 64 && m_tiles * ((N + Wide::bn - 1) / Wide::bn) >= kWideTiles) return shape_of<Wide>(M, 1);
-    const bool half = m_tiles * ((N + 127) / 128) * 4 < sms;
-    const int64_t tiles = m_tiles * (half ? (N + 63) / 64 : (N + 127) / 128);
-    int S = 1;
-    while (S < kMaxSplit && tiles * S * 2 <= 2 * sms && nk >= S * 4) S *= 2;
-    return half ? shape_of<Narrow64>(M, S) : shape_of<Narrow128>(M, S);
-}
-
+// What a form needs to know of the current device, found at its first call there: its kernel's
+// attributes are set, its registers checked, and the clusters of 2, 4 and 8 CTAs counted that
+// run at once (GPCs of uneven size hold fewer than SMs / S).
+struct Facts {
+    int clusters[4];  // of 1 << i CTAs
+};
 template <class F>
-uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p, int sms, bool overlap,
-                  cudaStream_t stream) {
-    static std::atomic<uint64_t> ready{0};  // devices on which the kernel's attributes are set and checked
+uno_status facts_of(int sms, Facts& f) {
+    static std::atomic<uint64_t> known[kDevices];  // 16 bits each for 1, 2, 4 and 8 CTAs; 0: not yet
     int dev = 0;
     uno_status s = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
     if (s != UNO_OK) return s;
-    const uint64_t bit = dev >= 0 && dev < kDevices ? 1ull << dev : 0ull;
-    if (!(ready.load(std::memory_order_acquire) & bit)) {
+    uint64_t k = dev < kDevices ? known[dev].load(std::memory_order_acquire) : 0;
+    if (!k) {
         s = check_cuda(cudaFuncSetAttribute(linear_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem),
                        "cudaFuncSetAttribute(fp8 linear)");
         cudaFuncAttributes a;
         if (s == UNO_OK) s = check_cuda(cudaFuncGetAttributes(&a, linear_kernel<F>), "cudaFuncGetAttributes(fp8 linear)");
         if (s != UNO_OK) return s;
         // the kernel's register split waits for what the launch did not bring
-        if (a.numRegs < F::regs)
+        if (F::split && a.numRegs < F::regs)
             return set_error(UNO_ERR_CUDA, "fp8 linear was built with %d registers a thread, %d are needed", a.numRegs,
                              F::regs);
-        ready.fetch_or(bit, std::memory_order_release);
+        k = (uint64_t)sms;
+        for (int i = 1; i < 4 && F::bn != Wide::bn; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 1u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.blockDim = dim3((unsigned)F::threads);
+            cfg.gridDim = dim3((unsigned)sms & ~7u);
+            cfg.dynamicSmemBytes = F::smem;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            s = check_cuda(cudaOccupancyMaxActiveClusters(&n, linear_kernel<F>, &cfg), "cudaOccupancyMaxActiveClusters");
+            if (s != UNO_OK) return s;
+            k |= (uint64_t)(n < 0xFFFF ? n : 0xFFFF) << (16 * i);
+        }
+        if (dev < kDevices) known[dev].store(k, std::memory_order_release);
     }
+    for (int i = 0; i < 4; ++i) f.clusters[i] = (int)(k >> (16 * i) & 0xFFFF);
+    return UNO_OK;
+}
+
+template <class F>
+uno_status narrow_shape(int64_t M, int64_t tiles, int nk, int sms, Shape& c) {
+    Facts f;
+    const uno_status s = facts_of<F>(sms, f);
+    if (s != UNO_OK) return s;
+    int i = 0;
+    while (i < 3 && tiles <= f.clusters[i + 1] && nk >= 4 << i) ++i;
+    c = shape_of<F>(M, 1 << i);
+    return UNO_OK;
+}
+
+uno_status choose(int64_t M, int64_t N, int nk, int sms, Shape& c) {
+    const int64_t m_tiles = (M + BM - 1) / BM;
+    if (M > 64 && m_tiles * ((N + Wide::bn - 1) / Wide::bn) >= kWideTiles) {
+        Facts f;
+        c = shape_of<Wide>(M, 1);
+        return facts_of<Wide>(sms, f);
+    }
+    if (m_tiles * ((N + 127) / 128) * 4 < sms)
+        return narrow_shape<Narrow64>(M, m_tiles * ((N + 63) / 64), nk, sms, c);
+    return narrow_shape<Narrow128>(M, m_tiles * ((N + 127) / 128), nk, sms, c);
+}
+
+template <class F>
+uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p, int sms, cudaStream_t stream) {
     // persistent, except where a cluster shares a tile
-    const int64_t most = (int64_t)sms * F::ctas;
-    const int64_t units = c.S > 1 || p.tiles < most ? p.tiles : most;
+    const int64_t units = c.S > 1 || p.tiles < sms ? p.tiles : sms;
     if (units * c.S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attrs[2];
+    cudaLaunchAttribute attr;
     cfg.blockDim = dim3((unsigned)F::threads);
     cfg.gridDim = dim3((unsigned)(units * c.S));
     cfg.dynamicSmemBytes = c.smem;
     cfg.stream = stream;
-    cfg.attrs = attrs;
+    cfg.attrs = &attr;
     if (c.S > 1) {
-        attrs[0].id = cudaLaunchAttributeClusterDimension;
-        attrs[0].val.clusterDim.x = (unsigned)c.S;
-        attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)c.S;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.numAttrs = 1;
-    }
-    if (overlap) {
-        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
     return check_cuda(cudaLaunchKernelEx(&cfg, linear_kernel<F>, maps[0], maps[1], maps[2], maps[3], p),
                       "launch(fp8 linear)");
@@ -796,13 +837,15 @@ uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p,
 
 // one product: e4m3 blocks over d_in columns (or none), bf16 blocks over r columns (or none)
 uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, const void* b, int64_t r, Params p,
-                   bool overlap, cudaStream_t stream) {
+                   cudaStream_t stream) {
     const int sms = device_sms();
     p.status = device_status_ptr();
     if (sms == 0 || !p.status) return set_error(UNO_ERR_CUDA, "the current device's properties cannot be read");
     p.nk8 = (int)((d_in + 127) / 128);
     p.nk16 = (int)((r + 63) / 64);
-    const Shape c = choose(p.M, p.N, p.nk8 + p.nk16, sms);
+    Shape c;
+    uno_status s = choose(p.M, p.N, p.nk8 + p.nk16, sms, c);
+    if (s != UNO_OK) return s;
     p.m_tiles = (p.M + BM - 1) / BM;
     p.stages = c.stages;
     p.a_rows = c.a_rows;
@@ -811,7 +854,6 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     if (tiles * (p.nk8 + p.nk16) > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     p.tiles = (int)tiles;
     CUtensorMap maps[4];
-    uno_status s = UNO_OK;
     if (d_in) {
         s = operand_map(&maps[0], xq, p.M, d_in, false, c.a_rows);
         if (s == UNO_OK) s = operand_map(&maps[1], wq, p.N, d_in, false, (uint32_t)c.BN);
@@ -823,9 +865,9 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     if (s != UNO_OK) return s;
     if (!d_in) maps[0] = maps[2], maps[1] = maps[3];  // (not read)
     if (!r) maps[2] = maps[0], maps[3] = maps[1];
-    return c.BN == Wide::bn        ? launch<Wide>(c, maps, p, sms, overlap, stream)
-           : c.BN == Narrow128::bn ? launch<Narrow128>(c, maps, p, sms, overlap, stream)
-                                   : launch<Narrow64>(c, maps, p, sms, overlap, stream);
+    return c.BN == Wide::bn        ? launch<Wide>(c, maps, p, sms, stream)
+           : c.BN == Narrow128::bn ? launch<Narrow128>(c, maps, p, sms, stream)
+                                   : launch<Narrow64>(c, maps, p, sms, stream);
 }
 
 }  // namespace fp8lin
@@ -874,7 +916,7 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
         fp8lin::Params t = p;
         t.N = (int)rank;
         t.y = workspace;
-        const uno_status s = fp8lin::product(nullptr, nullptr, 0, x, lora_a, d_in, t, false, st);
+        const uno_status s = fp8lin::product(nullptr, nullptr, 0, x, lora_a, d_in, t, st);
         if (s != UNO_OK) return s;
     }
     p.N = (int)d_out;
@@ -884,6 +926,5 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
     p.scale = scale;
     p.y = y;
     p.y_f32 = y_dtype == UNO_F32;
-    p.wait_t = adapter;
-    return fp8lin::product(x_q, w_q, d_in, workspace, lora_b, adapter ? rank : 0, p, adapter, st);
+    return fp8lin::product(x_q, w_q, d_in, workspace, lora_b, adapter ? rank : 0, p, st);
 }

@@ -173,8 +173,8 @@ def test_two_streams_dirty_workspaces_and_graphs():
 @pytest.mark.parametrize("M,d_in,d_out,rank", [(24, 512, 4000, 64), (16, 4096, 4096, 128), (40, 1024, 20000, 64),
                                                (200, 512, 9728, 64), (700, 1024, 9728, 128)])
 def test_the_adapter_reads_what_this_call_made(M, d_in, d_out, rank):
-    """The projection starts beside the kernel that makes T and waits for it: with the workspace
-    overwritten between calls, every call gives the first one's bits."""
+    """The projection reads the T that its own call made: with the workspace overwritten between
+    calls, every call gives the first one's bits."""
     c = _cuda(_operands(M, d_in, d_out, rank))
     ws = torch.empty(_lib.uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank), dtype=torch.uint8,
                      device="cuda")
@@ -183,6 +183,23 @@ def test_the_adapter_reads_what_this_call_made(M, d_in, d_out, rank):
     for _ in range(60):
         ws.fill_(0x45)
         assert torch.equal(_run(c, y, workspace=ws), first)
+
+
+@pytest.mark.parametrize("M,d_in,d_out,rank", [(210, 1632, 4448, 64), (4696, 1200, 432, 128), (7877, 1056, 1472, 8),
+                                               (195, 816, 584, 8)])
+def test_call_after_call(M, d_in, d_out, rank):
+    """Hundreds of calls on an idle GPU, each with the sums of its few K blocks joined by clusters or
+    its last row tile partly empty: the first one's bits every time, and no wait gives up."""
+    o = _operands(M, d_in, d_out, rank)
+    c = _cuda(o)
+    first = _run(c, torch.empty((M, d_out), dtype=BF, device="cuda"))
+    y = torch.empty_like(first)
+    for _ in range(400):
+        torch.cuda.synchronize()
+        assert torch.equal(_run(c, y), first)
+    assert _lib.uno_read_device_status() == _lib.UNO_OK
+    rows = torch.cat([torch.arange(8), torch.arange(M - 8, M)])
+    _check({k: (v[rows] if k in ("xq", "xs", "x", "gate") else v) for k, v in o.items()}, first[rows.cuda()])
 
 
 def test_same_bits_every_time():

@@ -9,7 +9,12 @@
 //   e4m3 block b:  acc += xs[m, b] ws[n / 128, b] * D        adapter:  acc += scale g[m] * D
 // so scales of any size cost one multiply-add per element and block, and the gate costs
 // nothing. T is made by the same kernel first: a product with adapter blocks alone (X, A) and
-// factor 1.
+// factor 1; the projection is launched to start on the SMs that this leaves free, and waits for
+// its end before it reads T (M 16, 4096 -> 4096, rank 128: 13.5 us, 19.1 one after the other).
+//
+// Bound: tensor cores for large M (M 8192, 2560 -> 9728: 216 us, 1885 TFLOP/s), HBM for few rows
+// of a wide head (M 64, 4096 -> 151936: 115 us, 5.6 TB/s), and between them the draining chain of
+// a tile's K blocks (M 16, 4096 -> 4096 without an adapter: 11 us for 17 MB).
 //
 // Roles of a CTA's warps: 0 loads K blocks by TMA into a ring of shared-memory stages; 1 and 2
 // issue tcgen05.mma for the even and the odd K blocks, each into accumulators of its own
@@ -58,6 +63,8 @@ struct Params {
     float scale;
     void* y;
     int y_f32;
+    int ahead;             // this call's next kernel may start before this one's end
+    int wait_t;            // T comes from the kernel before this one
     uint32_t* status;
 };
 
@@ -124,19 +131,6 @@ __device__ __forceinline__ void tmem_wait(float (&r)[16]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait(float (&r)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])
-                 :
-                 : "memory");
-}
-
 // True in one lane of a converged warp. The roles below run whole warps and issue under this
 // predicate: the compiler then keeps descriptors and addresses in uniform registers, which a
 // branch on the lane number denies it (a K block's four products issue in 150 clocks instead
@@ -154,17 +148,6 @@ __device__ __forceinline__ bool elect_one() {
 // a thousand clocks.
 __device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
     asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-__device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
-          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-        : "r"(taddr)
-        : "memory");
 }
 
 // four bytes from global to shared memory, asynchronously; and this thread's arrival at an
@@ -339,18 +322,20 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, co
 // BN: columns of a tile; EW: draining warps. One CTA per SM: that is all the runtime's occupancy
 // query allows this kernel, whatever its size. (Forms of half an SM, two of whose CTAs the
 // hardware did place on one, failed with "unspecified launch failure" once in some thousand
-// calls, on an SM that held two.) NB accumulators of BN columns share the SM's TMEM.
+// calls, on an SM that held two.) NB accumulators of BN columns share the SM's TMEM. The narrow
+// forms drain with eight warps, whose registers need no split: sixteen took 125 us against 115
+// for M 64, 4096 -> 151936, and 17.0 against 16.0 for M 512, 4096 -> 4096.
 // ---------------------------------------------------------------------------------------
 template <int BN, int EW>
 struct Form {
     static constexpr int bn = BN, threads = 32 * (kRoles + EW);
     static constexpr int CW = BN * 4 / EW;          // columns of a draining warp
-    static constexpr int C = CW / 2 < 16 ? CW / 2 : 16;  // columns read ahead: CW / C is even
+    static constexpr int C = 16;                    // columns read ahead: CW / C is even
     static constexpr int tmem = 512, NB = tmem / BN;
     static constexpr int halves = BN > kBlockCols ? BN / kBlockCols : 1;  // blocks of weight rows
     // registers a thread at launch, and after the split: the role warps give up theirs. The
     // split's sum may not exceed the launch's total.
-    static constexpr bool split = CW > 32;
+    static constexpr bool split = BN == 256;
     static constexpr int regs = 96, role_regs = 32, drain_regs = 112;
     static_assert(!split || 32 * kRoles * role_regs + 32 * EW * drain_regs <= threads * regs, "register split");
     static constexpr int factor_bytes = 2 * kChunk * (kFactorPitch + halves) * 4;
@@ -358,8 +343,8 @@ struct Form {
     static constexpr int smem = 226 * 1024 - factor_bytes - 768;
 };
 using Wide = Form<256, 16>;
-using Narrow128 = Form<128, 16>;
-using Narrow64 = Form<64, 16>;
+using Narrow128 = Form<128, 8>;
+using Narrow64 = Form<64, 8>;
 
 template <class F>
 __global__ void __launch_bounds__(F::threads, 1)
@@ -421,18 +406,25 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
+    // the projection may start on the SMs that this product of few CTAs leaves free (before it
+    // reads T it waits for this grid's end)
+    if (p.ahead) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp < kRoles) {
     if (F::split) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::role_regs));
     if (warp == 0) {
         const bool one = elect_one();
         uint32_t s = 0, ph = 1, got = 0;
-        bool ok = true;  // (a lane that has given up keeps the others company)
+        bool waited = !p.wait_t, ok = true;  // (a lane that has given up keeps the others company)
         for (int tile = tile0; tile < p.tiles; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = ok && (got < ST || wait_phase(&empty[s], ph, gave_up));
                 const bool low = kb >= p.nk8;
+                if (low && !waited) {
+                    asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;" ::: "memory");
+                    waited = true;
+                }
                 if (one && ok) {
                     mbar_arrive_expect_tx(&full[s], a_bytes + b_bytes);
                     const uint32_t a = ring + s * a_bytes, b = ring_b + s * b_bytes;
@@ -722,7 +714,10 @@ struct Shape {
     size_t smem;
 };
 
-constexpr int64_t kWideTiles = 100;
+// A turn of wide tiles takes as long as 8 / 5 turns of narrow ones. M 256, 2560 -> 9728, rank 64:
+// one turn of wide tiles 18.7 us, two of narrow ones 22.4. M 512, 4096 -> 4096: one of each, 21.3
+// against 16.0.
+constexpr int kWideCost = 8, kNarrowCost = 5;
 
 template <class F>
 Shape shape_of(int64_t M, int S) {
@@ -803,7 +798,8 @@ uno_status narrow_shape(int64_t M, int64_t tiles, int nk, int sms, Shape& c) {
 
 uno_status choose(int64_t M, int64_t N, int nk, int sms, Shape& c) {
     const int64_t m_tiles = (M + BM - 1) / BM;
-    if (M > 64 && m_tiles * ((N + Wide::bn - 1) / Wide::bn) >= kWideTiles) {
+    auto turns = [&](int bn) { return (m_tiles * ((N + bn - 1) / bn) + sms - 1) / sms; };
+    if (M > 64 && turns(Narrow128::bn) * kNarrowCost > turns(Wide::bn) * kWideCost) {
         Facts f;
         c = shape_of<Wide>(M, 1);
         return facts_of<Wide>(sms, f);
@@ -819,17 +815,21 @@ uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p,
     const int64_t units = c.S > 1 || p.tiles < sms ? p.tiles : sms;
     if (units * c.S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attrs[2];
     cfg.blockDim = dim3((unsigned)F::threads);
     cfg.gridDim = dim3((unsigned)(units * c.S));
     cfg.dynamicSmemBytes = c.smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
+    cfg.attrs = attrs;
     if (c.S > 1) {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = (unsigned)c.S;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = (unsigned)c.S;
+        attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
         cfg.numAttrs = 1;
+    }
+    if (p.wait_t) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
     return check_cuda(cudaLaunchKernelEx(&cfg, linear_kernel<F>, maps[0], maps[1], maps[2], maps[3], p),
                       "launch(fp8 linear)");
@@ -916,6 +916,7 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
         fp8lin::Params t = p;
         t.N = (int)rank;
         t.y = workspace;
+        t.ahead = 1;
         const uno_status s = fp8lin::product(nullptr, nullptr, 0, x, lora_a, d_in, t, st);
         if (s != UNO_OK) return s;
     }
@@ -926,5 +927,6 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
     p.scale = scale;
     p.y = y;
     p.y_f32 = y_dtype == UNO_F32;
+    p.wait_t = adapter;
     return fp8lin::product(x_q, w_q, d_in, workspace, lora_b, adapter ? rank : 0, p, st);
 }

@@ -45,7 +45,7 @@ extern "C" {
  *   out_q       [M, d] e4m3, out_scale [M, ceil(d/128)] float32; both or neither
  *   out_y       [M, d] dtype or NULL: y rounded to dtype (what an adapter reads)
  *
- * Sums of squares in float32. Limits (else UNO_ERR_UNSUPPORTED): d a multiple of 16, d <=
+ * Sums of squares in float32; a row whose sum passes its range comes out as NaN. Limits (else UNO_ERR_UNSUPPORTED): d a multiple of 16, d <=
  * 32768, M < 2^31. eps positive and finite; out_q or out_y has to be given; out_residual
  * needs residual. No workspace.
  * ====================================================================================== */
@@ -87,8 +87,9 @@ uno_status uno_fp8_quantize(const void* x, uno_dtype dtype, int64_t rows, int64_
  * accumulated in float32 and multiplied by scale * g. A row whose scale * g is 0 gets no
  * adapter term. Y is rounded once to y_dtype. Sums are taken in an order fixed by the sizes.
  *
- * Limits (else UNO_ERR_UNSUPPORTED): d_in a multiple of 16, d_in, <= 65536; d_out <= 2^20;
- * M <= 2^20; rank 0 or a multiple of 8 up to 256; y_dtype UNO_F32 only with rank 0.
+ * Limits (else UNO_ERR_UNSUPPORTED): d_in a multiple of 16, d_in <= 65536; d_out <= 2^20;
+ * M <= 2^20; rank 0 or a multiple of 8 up to 256; y_dtype UNO_F32 only with rank 0; output tiles
+ * of 128 x 256 (few rows: 128 x 128) times blocks of 128 columns below 2^31.
  * Workspace: uno_fp8_gated_lora_linear_workspace_size bytes (0 with rank 0: may be NULL).
  * ====================================================================================== */
 size_t uno_fp8_gated_lora_linear_workspace_size(int64_t M, int64_t d_in, int64_t d_out, int64_t rank);

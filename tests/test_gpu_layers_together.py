@@ -2,6 +2,8 @@
 8-bit base, head, verify, report of the emitted tokens and the gradient of their log
 probabilities, each stage held to its plain 64-bit form on the stage's own inputs; and the
 step driver on the 8-bit base, eager and as a graph."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -86,6 +88,8 @@ def test_a_step_of_a_model_with_an_8bit_base():
     _lib.uno_token_logprobs_grad(logits, tok.view(-1), st, grad, grad_logprob=torch.ones(M, device="cuda"))
     ref, _ = R.logprobs_grad(c(logits), tokens, 1.0, torch.ones(M))
     assert (c(grad)[tokens < 0] == 0).all()
+    # (the rounding to bf16 of the value; of the token's own, 1 - p, the float32 p's error of a few
+    # 2^-24 is absolute: below 1e-6)
     assert ((c(grad).double() - ref).abs() <= 1.02 * R.HALF_BF16 * ref.abs() + 1e-6).all()
     assert _lib.uno_read_device_status() == _lib.UNO_OK
 
@@ -94,6 +98,62 @@ V_ = W.VerifyWorkload("drv", 4242, B=4, K=16, V=32000, sigma=3.0, rho=0.8, tempe
 L_ = W.GatedLoraWorkload("drv", 4243, M=4 * 16, block=16, rank=16, scale=2.0,
                          shapes=(W.LinearShape("q", 512, 512), W.LinearShape("k", 512, 128), W.LinearShape("o", 512, 512),
                                  W.LinearShape("gate", 512, 1024), W.LinearShape("down", 1024, 512)))
+
+
+def test_two_host_threads_at_once():
+    """Two threads call the same entry points, each on a stream of its own, with other sizes: each
+    gets what it gets alone, and a refusal in one does not show in the other."""
+    def operands(M, d, V, seed):
+        g = torch.Generator().manual_seed(seed)
+        o = {"x": torch.randn((M, d), generator=g).to(BF).cuda(), "w": torch.ones(d, dtype=BF, device="cuda")}
+        w = (0.1 * torch.randn((V, d), generator=g)).to(BF).cuda()
+        o["w8"], o["ws"] = torch.empty((V, d), dtype=R.F8, device="cuda"), \
+            torch.empty((-(-V // 128), -(-d // 128)), device="cuda")
+        _lib.uno_fp8_quantize(w, o["w8"], o["ws"], 128)
+        o["a"], o["b"] = (0.1 * torch.randn((16, d), generator=g)).to(BF).cuda(), \
+            torch.randn((V, 16), generator=g).to(BF).cuda()
+        o["gate"], o["tok"] = torch.ones(M, device="cuda"), torch.arange(M, dtype=torch.int32, device="cuda")
+        return o
+
+    def run(o):
+        M, d = o["x"].shape
+        q, s = torch.empty((M, d), dtype=R.F8, device="cuda"), torch.empty((M, -(-d // 128)), device="cuda")
+        _lib.uno_rms_norm_fp8(o["x"], o["w"], 1e-6, q, s)
+        logits = torch.empty((M, o["w8"].shape[0]), dtype=BF, device="cuda")
+        _lib.uno_fp8_gated_lora_linear(q, s, o["w8"], o["ws"], logits, x=o["x"], lora_a=o["a"], lora_b=o["b"],
+                                       row_gate=o["gate"], scale=0.5)
+        lp, ent = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        _lib.uno_token_logprobs(logits, o["tok"], lp, 0.7, ent)
+        return logits, lp, ent
+
+    sets = [operands(40, 512, 3001, 1), operands(300, 1040, 1504, 2)]
+    alone = [run(o) for o in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def thread(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for n in range(60):
+                    got = run(sets[i])
+                    if i and n % 5 == 0:
+                        with pytest.raises(_lib.UnoError, match="temperature"):
+                            _lib.uno_token_logprobs(got[0], sets[i]["tok"], got[1], 0.0, got[2])
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, alone[i])):
+                        bad.append((i, n))
+                stream.synchronize()
+        except BaseException as e:  # noqa: BLE001 (reported below, by the test's own thread)
+            bad.append((i, repr(e)))
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:4]
+    assert _lib.uno_read_device_status() == _lib.UNO_OK
 
 
 def _steps(graph, base="fp8", report=5):
@@ -130,6 +190,8 @@ def test_driver_on_an_8bit_base():
             else:
                 q, s = R.quantize(x.double(), 1)
             assert torch.equal(o[f"q{i}"].double(), q)
+            # (roundings of 2^-24 in a scale: half of those in the sum of squares, at most d / 512 + 18
+            # on the way of one square, and six more; 16 of them at these widths)
             assert ((o[f"s{i}"].double() - s).abs() <= 2.0 ** -20 * s).all()
         for i, L in enumerate(d.lin):
             k = list(d.act8).index(L["act"])

@@ -17,6 +17,9 @@
 // counting, value first and id second: a long list first in shares, one for each warp. A list that overflows (a row in ascending order, a row of equal values) is
 // no loss: its entries are real tokens, so the top_n-th best of them bounds the search and the
 // run is read again for what beats it, until the list holds everything.
+// Measured: 2048 rows of 166144 bf16, 40% left out, 5 alternatives: 81-88 us, 4.6-5.0 TB/s; 16 rows
+// of 151936, 20 alternatives: 10.5 us (eight CTAs a row; ranking and joining take half). With its
+// gradient, 1024 rows of 151936: 161 us, the logits read twice and the gradient written once.
 #include <cmath>
 #include <type_traits>
 

@@ -54,7 +54,8 @@ constexpr int kFactorPitch = BM + 4; // floats of a K block's row factors (write
 struct Params {
     int M, N;              // rows and columns of Y
     int nk8, nk16;         // K blocks of e4m3 and of bf16
-    int m_tiles, tiles;    // row tiles, all tiles
+    int m_tiles;           // row tiles
+    int first, tiles;      // this launch's tiles: first .. tiles - 1
     int stages;
     uint32_t a_rows;       // rows of x loaded per K block (a multiple of 8, at most 128)
     const float* xs;       // [M, nk8]
@@ -64,7 +65,7 @@ struct Params {
     void* y;
     int y_f32;
     int ahead;             // this call's next kernel may start before this one's end
-    int wait_t;            // T comes from the kernel before this one
+    int after;             // started so: waits for the end of the one before, where T comes from
     uint32_t* status;
 };
 
@@ -371,7 +372,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* gave_up = &s_gave_up;
     const uint32_t S = F::bn == 256 ? 1u : cluster_size(), rank = F::bn == 256 ? 0u : cluster_rank();
-    const int tile0 = blockIdx.x / S, step = gridDim.x / S;
+    const int tile0 = p.first + blockIdx.x / S, step = gridDim.x / S;
     // this CTA's share of the K blocks of its tiles
     const int nk = p.nk8 + p.nk16;
     const int kb0 = (int)((int64_t)nk * rank / S), kb1 = (int)((int64_t)nk * (rank + 1) / S);
@@ -406,8 +407,8 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
-    // the projection may start on the SMs that this product of few CTAs leaves free (before it
-    // reads T it waits for this grid's end)
+    // this call's next kernel may start on the SMs that this one of few CTAs leaves free (before it
+    // reads T, and before it ends, it waits for this grid's end)
     if (p.ahead) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp < kRoles) {
@@ -415,7 +416,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
     if (warp == 0) {
         const bool one = elect_one();
         uint32_t s = 0, ph = 1, got = 0;
-        bool waited = !p.wait_t, ok = true;  // (a lane that has given up keeps the others company)
+        bool waited = !p.after, ok = true;  // (a lane that has given up keeps the others company)
         for (int tile = tile0; tile < p.tiles; tile += step) {
             const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -444,6 +445,8 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                 }
             }
         }
+        // (what follows on the stream waits for this grid only)
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
         // Nothing may still be on its way to this CTA's shared memory when it ends: the last commits
         // arrive at `empty` on their own, after the accumulators they follow have been seen (an
         // arrival at the barriers of the next CTA in this place would break its ring). Loads that
@@ -812,7 +815,7 @@ uno_status choose(int64_t M, int64_t N, int nk, int sms, Shape& c) {
 template <class F>
 uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p, int sms, cudaStream_t stream) {
     // persistent, except where a cluster shares a tile
-    const int64_t units = c.S > 1 || p.tiles < sms ? p.tiles : sms;
+    const int64_t tiles = p.tiles - p.first, units = c.S > 1 || tiles < sms ? tiles : sms;
     if (units * c.S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attrs[2];
@@ -827,7 +830,7 @@ uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p,
         attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
         cfg.numAttrs = 1;
     }
-    if (p.wait_t) {
+    if (p.after) {
         attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
@@ -847,27 +850,55 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     uno_status s = choose(p.M, p.N, p.nk8 + p.nk16, sms, c);
     if (s != UNO_OK) return s;
     p.m_tiles = (p.M + BM - 1) / BM;
-    p.stages = c.stages;
-    p.a_rows = c.a_rows;
+    const int nk = p.nk8 + p.nk16;
     const int64_t tiles = (int64_t)p.m_tiles * ((p.N + c.BN - 1) / c.BN);
     // (K blocks are counted over a CTA's tiles in 32 bits)
-    if (tiles * (p.nk8 + p.nk16) > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
+    if (tiles * nk > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     p.tiles = (int)tiles;
-    CUtensorMap maps[4];
-    if (d_in) {
-        s = operand_map(&maps[0], xq, p.M, d_in, false, c.a_rows);
-        if (s == UNO_OK) s = operand_map(&maps[1], wq, p.N, d_in, false, (uint32_t)c.BN);
+    auto run = [&](const Shape& c, Params p) {
+        p.stages = c.stages;
+        p.a_rows = c.a_rows;
+        CUtensorMap maps[4];
+        uno_status s = UNO_OK;
+        if (d_in) {
+            s = operand_map(&maps[0], xq, p.M, d_in, false, c.a_rows);
+            if (s == UNO_OK) s = operand_map(&maps[1], wq, p.N, d_in, false, (uint32_t)c.BN);
+        }
+        if (s == UNO_OK && r) {
+            s = operand_map(&maps[2], t, p.M, r, true, c.a_rows);
+            if (s == UNO_OK) s = operand_map(&maps[3], b, p.N, r, true, (uint32_t)c.BN);
+        }
+        if (s != UNO_OK) return s;
+        if (!d_in) maps[0] = maps[2], maps[1] = maps[3];  // (not read)
+        if (!r) maps[2] = maps[0], maps[3] = maps[1];
+        return c.BN == Wide::bn        ? launch<Wide>(c, maps, p, sms, stream)
+               : c.BN == Narrow128::bn ? launch<Narrow128>(c, maps, p, sms, stream)
+                                       : launch<Narrow64>(c, maps, p, sms, stream);
+    };
+    // The persistent CTAs' last turn may hold few tiles (a head of 151936 columns has 1187 of 128
+    // columns for 148 SMs: eight turns and three tiles). Then the last columns' tiles are shared by
+    // clusters of eight in a launch of their own, and the others start beside it: M 128, 4096 ->
+    // 151936 123 us in place of 132, M 64 119.7 in place of 121.1, M 8, 4096 -> 19200 24.4 in place
+    // of 27.6. Not with more tiles or fewer K blocks: M 2000, 2048 -> 9728 (32 tiles) 68 against 60,
+    // M 16, 2560 -> 151936 75.2 against 73.9.
+    if (c.S == 1 && tiles > sms && nk >= 32) {
+        Facts f;
+        s = facts_of<Narrow128>(sms, f);
+        if (s != UNO_OK) return s;
+        const int64_t whole = tiles / sms * sms / p.m_tiles * (c.BN / Narrow128::bn);  // columns of narrow tiles
+        const int64_t rest = p.m_tiles * ((p.N + Narrow128::bn - 1) / Narrow128::bn - whole);
+        if (rest > 0 && rest <= f.clusters[3]) {
+            Params last = p;
+            last.first = (int)(p.m_tiles * whole);
+            last.tiles = (int)(last.first + rest);
+            last.ahead = 1;
+            s = run(shape_of<Narrow128>(p.M, 8), last);
+            if (s != UNO_OK) return s;
+            p.tiles = (int)(p.m_tiles * (whole / (c.BN / Narrow128::bn)));
+            p.after = 1;
+        }
     }
-    if (s == UNO_OK && r) {
-        s = operand_map(&maps[2], t, p.M, r, true, c.a_rows);
-        if (s == UNO_OK) s = operand_map(&maps[3], b, p.N, r, true, (uint32_t)c.BN);
-    }
-    if (s != UNO_OK) return s;
-    if (!d_in) maps[0] = maps[2], maps[1] = maps[3];  // (not read)
-    if (!r) maps[2] = maps[0], maps[3] = maps[1];
-    return c.BN == Wide::bn        ? launch<Wide>(c, maps, p, sms, stream)
-           : c.BN == Narrow128::bn ? launch<Narrow128>(c, maps, p, sms, stream)
-                                   : launch<Narrow64>(c, maps, p, sms, stream);
+    return run(c, p);
 }
 
 }  // namespace fp8lin
@@ -927,6 +958,6 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
     p.scale = scale;
     p.y = y;
     p.y_f32 = y_dtype == UNO_F32;
-    p.wait_t = adapter;
+    p.after = adapter;
     return fp8lin::product(x_q, w_q, d_in, workspace, lora_b, adapter ? rank : 0, p, st);
 }

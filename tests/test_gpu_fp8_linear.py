@@ -185,6 +185,33 @@ def test_the_adapter_reads_what_this_call_made(M, d_in, d_out, rank):
         assert torch.equal(_run(c, y, workspace=ws), first)
 
 
+@pytest.mark.parametrize("M,d_in,d_out,rank,dtype", [(16, 4096, 19067, 0, F32), (40, 4112, 19200, 64, BF),
+                                                     (1, 4096, 37900, 0, BF), (200, 4096, 19184, 8, BF),
+                                                     (642, 4096, 12584, 16, BF), (514, 4096, 15139, 0, F32)])
+def test_last_columns_in_a_launch_of_their_own(M, d_in, d_out, rank, dtype):
+    """Tiles for a few turns of the SMs and a little more: every element is written, by the launch of
+    the last columns or the one beside it, and nothing on the stream runs before both have ended."""
+    o = _operands(M, d_in, d_out, rank)
+    c = _cuda(o)
+    y = torch.full((M, d_out), math.nan, dtype=dtype, device="cuda")
+    first = _run(c, y).clone()
+    assert torch.isfinite(first).all()
+    rows = torch.unique(torch.cat([torch.arange(min(M, 8)), torch.arange(max(0, M - 8), M)]))
+    _check({k: (v[rows] if k in ("xq", "xs", "x", "gate") else v) for k, v in o.items()}, first[rows.cuda()])
+    for _ in range(20):
+        y.fill_(math.nan)
+        assert torch.equal(_run(c, y), first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y.fill_(math.nan)
+        _run(c, y)
+        copy = y.clone()
+    for _ in range(5):
+        graph.replay()
+        assert torch.equal(copy, first)
+    assert _lib.uno_read_device_status() == _lib.UNO_OK
+
+
 @pytest.mark.parametrize("M,d_in,d_out,rank", [(210, 1632, 4448, 64), (4696, 1200, 432, 128), (7877, 1056, 1472, 8),
                                                (195, 816, 584, 8)])
 def test_call_after_call(M, d_in, d_out, rank):

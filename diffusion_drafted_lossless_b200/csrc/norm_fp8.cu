@@ -21,7 +21,7 @@
 // bytes a thread at a time, read back by the thread that wrote them). One CTA per row.
 // Measured: the norm of 16384 x 2560 bf16 with a residual 51 us, 5.8 TB/s; 16 x 4096 2.3 us (one
 // row's latency); the quantiser on 1024 x 12288 float32 14.0 us, 4.5 TB/s, and on 9728 x 2560 bf16
-// by 128 x 128 blocks 18.5 us, 4.0 TB/s (sizes near that of L2, a launch's ramp in each).
+// by 128 x 128 blocks 14.2 us, 5.3 TB/s (sizes near that of L2, a launch's ramp in each).
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -183,14 +183,15 @@ __device__ __forceinline__ void scaled2(float u0, float u1, float c, float r, fl
 }
 
 // The same for u that float32 holds exactly. EXACT: 448 u / a is known not to lie within
-// 2^-24 of a border of e4m3 without being on it (see above).
-template <bool EXACT>
+// 2^-24 of a border of e4m3 without being on it (see above). ORDINARY: a is known to be far from
+// overflow and underflow.
+template <bool EXACT, bool ORDINARY = false>
 __device__ __forceinline__ float quotients(const float (&u)[V], float a, float factor, float (&t)[V]) {
     // a factor / 448, the 1 / 448 as a float32 and its remainder (one rounding where factor is 1)
     constexpr float hi = (float)(1.0 / 448.0), lo = (float)(1.0 / 448.0 - (double)hi);
     const float y = a * factor, scale = fmaf(y, hi, y * lo);
     // far from overflow and underflow of 448 / a and its remainder
-    if (a >= 0x1p-90f && a <= 0x1p90f && scale >= kMinScale) {
+    if (ORDINARY || (a >= 0x1p-90f && a <= 0x1p90f && scale >= kMinScale)) {
         const float inv = reciprocal(a), c = kE4m3Max * inv;
         const float r = fmaf(-c, a, kE4m3Max) * inv;  // 448 / a - c, to 20 bits and more
 #pragma unroll
@@ -396,12 +397,19 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
     }
 }
 
-// 128 x 128 blocks: a CTA of 16 warps holds one in registers, four pieces a thread
+// 128 x 128 blocks: a CTA holds one in registers, four or eight pieces a thread. Its loads, its
+// maximum and its stores come one after the other, so other CTAs have to fill the gaps: three of
+// 256 threads an SM take 14.2 us for 9728 x 2560 bf16, two of 512 16.8 (float32, whose pieces take
+// twice the registers: two of 512 23.4, of 256 26.9).
 template <typename T>
-__global__ void __launch_bounds__(512, 2) quantize_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
+constexpr int kBlockThreads = std::is_same_v<T, float> ? 512 : 256;
+template <typename T>
+constexpr int kBlockCtas = std::is_same_v<T, float> ? 2 : 3;  // per SM, as registers allow
+template <typename T>
+__global__ void __launch_bounds__(kBlockThreads<T>, kBlockCtas<T>) quantize_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
                                                               uint8_t* __restrict__ q, float* __restrict__ scale) {
-    constexpr int N = 128 * kLanes / 512;
-    __shared__ float part[16];
+    constexpr int NT = kBlockThreads<T>, N = 128 * kLanes / NT;
+    __shared__ float part[NT / 32];
     const int64_t nblocks = (cols + kBlockCols - 1) / kBlockCols;
     const int64_t rb = blockIdx.x / nblocks, cb = blockIdx.x - rb * nblocks;
     const int64_t col = cb * kBlockCols + (threadIdx.x % kLanes) * V, row0 = rb * 128 + threadIdx.x / kLanes;
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(512, 2) quantize_blocks_kernel(const T* __rest
     float a = 0.f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int64_t row = row0 + k * (512 / kLanes);
+        const int64_t row = row0 + k * (NT / kLanes);
         v[k] = row < rows && col < cols ? stream_piece(x + row * cols + col) : zero_piece<T>();
     }
 #pragma unroll
@@ -421,16 +429,23 @@ __global__ void __launch_bounds__(512, 2) quantize_blocks_kernel(const T* __rest
     a = warp_max(a);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
     __syncthreads();
-    a = warp_max(part[threadIdx.x & 15]);
+    a = warp_max(part[threadIdx.x & (NT / 32 - 1)]);
+    uint8_t* out = q + row0 * cols + col;
+    const bool in = col < cols;
+    const int left = in ? (int)(rows - row0 < 128 ? rows - row0 : 128) : 0;  // of this thread's rows
+    auto each = [&](auto ordinary) {
+        float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int64_t row = row0 + k * (512 / kLanes);
-        float f[V], t[V];
-        unpack<T>(v[k], f);
-        const float s = quotients<!std::is_same_v<T, float>>(f, a, 1.0f, t);
-        if (row < rows && col < cols) *reinterpret_cast<uint2*>(q + row * cols + col) = values(t);
-        if (k == 0 && threadIdx.x == 0) scale[rb * nblocks + cb] = s;
-    }
+        for (int k = 0; k < N; ++k) {
+            float f[V], t[V];
+            unpack<T>(v[k], f);
+            s = quotients<!std::is_same_v<T, float>, decltype(ordinary)::value>(f, a, 1.0f, t);
+            if (k * (NT / kLanes) < left) *reinterpret_cast<uint2*>(out + k * (NT / kLanes) * cols) = values(t);
+        }
+        if (threadIdx.x == 0) scale[rb * nblocks + cb] = s;
+    };
+    if (a >= 0x1p-90f && a <= 0x1p90f) each(std::true_type{});
+    else each(std::false_type{});
 }
 
 template <typename T>
@@ -472,7 +487,7 @@ uno_status quantize_launch(const void* x, int64_t rows, int64_t cols, int block_
     } else {
         const int64_t blocks = ((rows + 127) / 128) * ((cols + kBlockCols - 1) / kBlockCols);
         if (blocks > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "more than 2^31 - 1 blocks");
-        quantize_blocks_kernel<T><<<(unsigned)blocks, 512, 0, stream>>>(static_cast<const T*>(x), rows, cols,
+        quantize_blocks_kernel<T><<<(unsigned)blocks, kBlockThreads<T>, 0, stream>>>(static_cast<const T*>(x), rows, cols,
                                                                        static_cast<uint8_t*>(q), scale);
     }
     return check_cuda(cudaGetLastError(), "launch(fp8 quantize)");

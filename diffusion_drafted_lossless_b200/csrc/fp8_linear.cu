@@ -788,18 +788,26 @@ uno_status facts_of(int sms, Facts& f) {
     return UNO_OK;
 }
 
+// The narrow form F of a product: CTAs per tile, and the K blocks that a CTA takes in turn (what
+// such a call's time goes by). `beside` CTAs of the kernel before may still hold SMs, and a cluster
+// that finds no place waits for them all: where they are few, clusters are counted without them.
 template <class F>
-uno_status narrow_shape(int64_t M, int64_t tiles, int nk, int sms, Shape& c) {
+uno_status narrow_shape(int64_t M, int64_t N, int nk, int sms, int beside, Shape& c, int64_t& in_turn) {
     Facts f;
     const uno_status s = facts_of<F>(sms, f);
     if (s != UNO_OK) return s;
+    const int64_t tiles = (M + BM - 1) / BM * ((N + F::bn - 1) / F::bn);
+    if (beside * 4 <= sms)
+        for (int& n : f.clusters) n = n * (sms - beside) / sms;
     int i = 0;
     while (i < 3 && tiles <= f.clusters[i + 1] && nk >= 4 << i) ++i;
+    in_turn = (tiles + sms - 1) / sms * ((nk + (1 << i) - 1) >> i);
+    if (i > 0) in_turn = (nk + (1 << i) - 1) >> i;
     c = shape_of<F>(M, 1 << i);
     return UNO_OK;
 }
 
-uno_status choose(int64_t M, int64_t N, int nk, int sms, Shape& c) {
+uno_status choose(int64_t M, int64_t N, int nk, int sms, int beside, Shape& c) {
     const int64_t m_tiles = (M + BM - 1) / BM;
     auto turns = [&](int bn) { return (m_tiles * ((N + bn - 1) / bn) + sms - 1) / sms; };
     if (M > 64 && turns(Narrow128::bn) * kNarrowCost > turns(Wide::bn) * kWideCost) {
@@ -807,9 +815,15 @@ uno_status choose(int64_t M, int64_t N, int nk, int sms, Shape& c) {
         c = shape_of<Wide>(M, 1);
         return facts_of<Wide>(sms, f);
     }
-    if (m_tiles * ((N + 127) / 128) * 4 < sms)
-        return narrow_shape<Narrow64>(M, m_tiles * ((N + 63) / 64), nk, sms, c);
-    return narrow_shape<Narrow128>(M, m_tiles * ((N + 127) / 128), nk, sms, c);
+    // The form with fewer K blocks in turn; M 16, 4096 -> 4096: 8 with 128 columns and clusters of
+    // four, 8.3 us, 16 with 64 columns and clusters of two, 10.9. Where both have as many, the one
+    // whose block is shorter: M 37, 4992 -> 700: 64 columns 6.9 us, 128 columns 7.4.
+    Shape c64;
+    int64_t in_turn, in_turn64;
+    uno_status s = narrow_shape<Narrow128>(M, N, nk, sms, beside, c, in_turn);
+    if (s == UNO_OK) s = narrow_shape<Narrow64>(M, N, nk, sms, beside, c64, in_turn64);
+    if (s == UNO_OK && in_turn64 <= in_turn) c = c64;
+    return s;
 }
 
 template <class F>
@@ -840,14 +854,14 @@ uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p,
 
 // one product: e4m3 blocks over d_in columns (or none), bf16 blocks over r columns (or none)
 uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, const void* b, int64_t r, Params p,
-                   cudaStream_t stream) {
+                   cudaStream_t stream, int beside, int* ctas) {
     const int sms = device_sms();
     p.status = device_status_ptr();
     if (sms == 0 || !p.status) return set_error(UNO_ERR_CUDA, "the current device's properties cannot be read");
     p.nk8 = (int)((d_in + 127) / 128);
     p.nk16 = (int)((r + 63) / 64);
     Shape c;
-    uno_status s = choose(p.M, p.N, p.nk8 + p.nk16, sms, c);
+    uno_status s = choose(p.M, p.N, p.nk8 + p.nk16, sms, beside, c);
     if (s != UNO_OK) return s;
     p.m_tiles = (p.M + BM - 1) / BM;
     const int nk = p.nk8 + p.nk16;
@@ -855,6 +869,7 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     // (K blocks are counted over a CTA's tiles in 32 bits)
     if (tiles * nk > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     p.tiles = (int)tiles;
+    if (ctas) *ctas = (int)(c.S > 1 || tiles < sms ? tiles * c.S : sms);
     auto run = [&](const Shape& c, Params p) {
         p.stages = c.stages;
         p.a_rows = c.a_rows;
@@ -881,7 +896,7 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     // 151936 123 us in place of 132, M 64 119.7 in place of 121.1, M 8, 4096 -> 19200 24.4 in place
     // of 27.6. Not with more tiles or fewer K blocks: M 2000, 2048 -> 9728 (32 tiles) 68 against 60,
     // M 16, 2560 -> 151936 75.2 against 73.9.
-    if (c.S == 1 && tiles > sms && nk >= 32) {
+    if (c.S == 1 && c.BN >= Narrow128::bn && tiles > sms && nk >= 32) {
         Facts f;
         s = facts_of<Narrow128>(sms, f);
         if (s != UNO_OK) return s;
@@ -943,12 +958,13 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     fp8lin::Params p{};
     p.M = (int)M;
-    if (adapter) {  // T = bf16(X A^T)
+    int beside = 0;  // CTAs that make T
+    if (adapter) {   // T = bf16(X A^T)
         fp8lin::Params t = p;
         t.N = (int)rank;
         t.y = workspace;
         t.ahead = 1;
-        const uno_status s = fp8lin::product(nullptr, nullptr, 0, x, lora_a, d_in, t, st);
+        const uno_status s = fp8lin::product(nullptr, nullptr, 0, x, lora_a, d_in, t, st, 0, &beside);
         if (s != UNO_OK) return s;
     }
     p.N = (int)d_out;
@@ -959,5 +975,5 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
     p.y = y;
     p.y_f32 = y_dtype == UNO_F32;
     p.after = adapter;
-    return fp8lin::product(x_q, w_q, d_in, workspace, lora_b, adapter ? rank : 0, p, st);
+    return fp8lin::product(x_q, w_q, d_in, workspace, lora_b, adapter ? rank : 0, p, st, beside, nullptr);
 }

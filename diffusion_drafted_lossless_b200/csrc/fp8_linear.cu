@@ -714,7 +714,6 @@ struct Shape {
     int S;       // CTAs per tile
     int stages;
     uint32_t a_rows;
-    size_t smem;
 };
 
 // A turn of wide tiles takes as long as 8 / 5 turns of narrow ones. M 256, 2560 -> 9728, rank 64:
@@ -731,14 +730,10 @@ Shape shape_of(int64_t M, int S) {
     const size_t stage = (size_t)(c.a_rows + F::bn) * kRowBytes;
     c.stages = (int)((F::smem - 1024) / stage);
     if (c.stages > kMaxStages) c.stages = kMaxStages;
-    size_t need = (size_t)c.stages * stage;
-    // the product reads 128 rows of x from every stage, loaded or not
-    const size_t reach = (size_t)(c.stages - 1) * c.a_rows * kRowBytes + BM * kRowBytes;
-    const size_t sums = S > 1 ? (size_t)BM * (F::bn + 4) * 4 : 0;
-    const size_t least = 120 * 1024;  // more than half an SM's: one CTA on each
-    for (const size_t n : {reach, sums, least})
-        if (need < n) need = n;
-    c.smem = need + 1024;
+    // (A launch takes all of the SM's shared memory, whatever the ring needs: no other CTA with TMEM
+    // of its own, this kernel's or another's, fits beside. The products read 128 rows of x from
+    // every stage, loaded or not, and a cluster's sums lie over the ring: both end inside it.)
+    static_assert(F::smem >= 1024 + BM * (F::bn + 4) * 4 || F::bn == 256, "a cluster's sums");
     return c;
 }
 
@@ -835,7 +830,7 @@ uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p,
     cudaLaunchAttribute attrs[2];
     cfg.blockDim = dim3((unsigned)F::threads);
     cfg.gridDim = dim3((unsigned)(units * c.S));
-    cfg.dynamicSmemBytes = c.smem;
+    cfg.dynamicSmemBytes = F::smem;
     cfg.stream = stream;
     cfg.attrs = attrs;
     if (c.S > 1) {

@@ -825,7 +825,6 @@ template <class F>
 uno_status launch(const Shape& c, const CUtensorMap (&maps)[4], const Params& p, int sms, cudaStream_t stream) {
     // persistent, except where a cluster shares a tile
     const int64_t tiles = p.tiles - p.first, units = c.S > 1 || tiles < sms ? tiles : sms;
-    if (units * c.S > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attrs[2];
     cfg.blockDim = dim3((unsigned)F::threads);
@@ -861,8 +860,6 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
     p.m_tiles = (p.M + BM - 1) / BM;
     const int nk = p.nk8 + p.nk16;
     const int64_t tiles = (int64_t)p.m_tiles * ((p.N + c.BN - 1) / c.BN);
-    // (K blocks are counted over a CTA's tiles in 32 bits)
-    if (tiles * nk > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     p.tiles = (int)tiles;
     if (ctas) *ctas = (int)(c.S > 1 || tiles < sms ? tiles * c.S : sms);
     auto run = [&](const Shape& c, Params p) {
@@ -932,6 +929,10 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
         return set_error(UNO_ERR_UNSUPPORTED, "d_in a multiple of 16 up to 65536, d_out and M up to 2^20 are supported");
     if (rank % 8 || rank > 256) return set_error(UNO_ERR_UNSUPPORTED, "rank must be 0 or a multiple of 8 and <= 256");
     if (rank && y_dtype == UNO_F32) return set_error(UNO_ERR_UNSUPPORTED, "float32 output is supported with rank 0");
+    // tiles times K blocks: they are counted over a CTA's tiles in 32 bits
+    if ((M + 127) / 128 * (M > 64 ? (d_out + 255) / 256 : (d_out + 127) / 128) * ((d_in + 127) / 128 + (rank + 63) / 64) >
+        0x7FFFFFFF)
+        return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     if (M == 0) return UNO_OK;
     if (!x_q || !x_scale || !w_q || !w_scale || !y) return set_error(UNO_ERR_INVALID_ARG, "a tensor pointer is NULL");
     if (rank && (!x || !lora_a || !lora_b)) return set_error(UNO_ERR_INVALID_ARG, "rank > 0 needs x, lora_a and lora_b");

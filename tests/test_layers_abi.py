@@ -66,6 +66,7 @@ def test_linear_refusals(lib):
     assert call(dt=3) == ARG and call(M=-1) == ARG and call(i=0) == ARG and call(o=0) == ARG and call(r=-8) == ARG
     assert call(i=264) == UNSUP and call(i=65536 + 16) == UNSUP and call(o=(1 << 20) + 1) == UNSUP
     assert call(M=(1 << 20) + 1) == UNSUP and call(r=12) == UNSUP and call(r=264) == UNSUP
+    assert call(M=1 << 20, i=65536, o=1 << 20) == UNSUP  # 8192 * 4096 tiles * 513 K blocks
     assert call(dt=1) == UNSUP  # float32 output with an adapter
     for k in ("xq", "xs", "wq", "ws", "y", "x", "a", "b"):
         assert call(**{k: None}) == ARG, k

@@ -267,6 +267,7 @@ def _current_stream(index: int) -> int:
 # (torch's own accessor of the handle, without the Stream object, where this torch has it: a
 # microsecond of a small call)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(fn, index, stream, *args):
@@ -278,7 +279,7 @@ def _call(fn, index, stream, *args):
         raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
     else:
         handle = stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -339,7 +340,7 @@ def uno_fp8_gated_lora_linear(x_q, x_scale, w_q, w_scale, y, x=None, lora_a=None
     if rank:
         nb = uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank)
         if workspace is None:
-            workspace = x_q.new_empty(nb, dtype=torch.uint8)
+            workspace = lora_a.new_empty(nb >> 1)  # (bf16; nb is a multiple of 256 bytes)
             if stream is not None and nb:
                 workspace.record_stream(stream)  # not handed out again before this stream is done with it
         elif workspace.get_device() != i:

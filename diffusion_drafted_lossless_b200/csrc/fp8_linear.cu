@@ -882,13 +882,13 @@ uno_status product(const void* xq, const void* wq, int64_t d_in, const void* t, 
                : c.BN == Narrow128::bn ? launch<Narrow128>(c, maps, p, sms, stream)
                                        : launch<Narrow64>(c, maps, p, sms, stream);
     };
-    // The persistent CTAs' last turn may hold few tiles (a head of 151936 columns has 1187 of 128
-    // columns for 148 SMs: eight turns and three tiles). Then the last columns' tiles are shared by
+    // The persistent CTAs' last turn may hold few tiles (a head of 151936 columns has 594 of 256
+    // columns for 148 SMs: four turns and two tiles). Then the last columns' tiles are shared by
     // clusters of eight in a launch of their own, and the others start beside it: M 128, 4096 ->
-    // 151936 123 us in place of 132, M 64 119.7 in place of 121.1, M 8, 4096 -> 19200 24.4 in place
-    // of 27.6. Not with more tiles or fewer K blocks: M 2000, 2048 -> 9728 (32 tiles) 68 against 60,
-    // M 16, 2560 -> 151936 75.2 against 73.9.
-    if (c.S == 1 && c.BN >= Narrow128::bn && tiles > sms && nk >= 32) {
+    // 151936 123 us in place of 132, M 8, 4096 -> 19200 (one turn) 24 in place of 28. Not with more
+    // tiles (M 2000, 2048 -> 9728, 32 tiles: 68 against 60), fewer K blocks (M 16, 2560 -> 151936:
+    // 75.2 against 73.9) or more turns (M 64, 4096 -> 151936, eight: 119.7 us either way).
+    if (c.S == 1 && c.BN >= Narrow128::bn && tiles > sms && tiles / sms <= 4 && nk >= 32) {
         Facts f;
         s = facts_of<Narrow128>(sms, f);
         if (s != UNO_OK) return s;

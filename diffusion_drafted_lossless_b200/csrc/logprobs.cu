@@ -3,8 +3,8 @@
 //
 //   s = sum exp((x - ref) / T),  a = sum exp((x - ref) / T) (x - ref)    (ref: near the maximum)
 //   log p_v = (x_v - max) / T - log s_max,   entropy = log s_max - a_max / (s_max T)
-// where s_max, a_max are the sums moved to ref = max. exp is ex2 of (x - ref) (log2 e / T);
-// x - ref is taken before the product, so values of any size keep their differences.
+// where s_max, a_max are the sums moved to ref = max. exp is ex2 of (x - ref) (log2 e / T), as
+// Sums below says for values and temperatures of every size.
 //
 // One pass over the row (bound: HBM, then the exponential unit: one ex2 an element). A row goes
 // to a cluster of S CTAs, each with a run of it; a thread streams 16-byte pieces, four added up
@@ -111,21 +111,28 @@ __device__ __forceinline__ float pieces_max(const uint4 (&v)[N]) {
     return fmaxf(m, -INFINITY);
 }
 
+// (x - ref) / T in octaves, c4 being 4 log2 e / T: a quarter of the difference, which is always
+// within float32, rounded once, and the product.
+__device__ __forceinline__ float octaves(float x, float ref, float c4) { return fmaf(x, 0.25f, -0.25f * ref) * c4; }
+
 // A thread's running sums over what it has read, in octaves: s = sum 2^arg, a = sum 2^arg arg.
-// Beside an ordinary reference (below 1e30 in size, the temperature below 1e20) arg is x c - R in
-// one rounding, R = ref c, and values below -1e30, -inf among them, count as -1e30: no weight
-// either way, and nothing overflows. Beside any other reference arg is (x - ref) c, and the two
-// kinds of sums never meet: the weights of one vanish beside the other's.
+// Beside an ordinary reference arg is x c - R in one rounding, R = ref c as float32 holds it.
+// R is off by half a unit of its own, the same for every element, and moving to another
+// reference takes that back; below 2^20 octaves it is at most a sixteenth, so no weight near the
+// maximum's overflows or is lost. Values below -1e30, -inf among them, count as -1e30: with c
+// between 1e-20 and 1e8 that is 1e10 octaves below any ordinary reference at least, and 1e38 at
+// most, in float32's range. Beside any other reference, or with any other c, arg is
+// octaves(x, ref), a subtraction and an instruction more an element.
 struct Sums {
     float ref, R, max, s, a;
     bool ordinary;
 };
-constexpr float kLow = -1e30f;
+constexpr float kLow = -1e30f, kMinC = 1.5e-20f, kMaxC = 1e8f, kMaxR = 1048576.f;
 
 __device__ __forceinline__ void set_ref(Sums& t, float ref, float c, bool plain) {
     t.ref = ref;
     t.R = ref * c;
-    t.ordinary = plain && fabsf(ref) < 1e30f;
+    t.ordinary = plain && fabsf(t.R) < kMaxR;
 }
 
 // the sums times 2^d, for a reference d octaves further up
@@ -135,18 +142,22 @@ __device__ __forceinline__ void shift(Sums& t, float d) {
     t.s *= f;
 }
 
+// how many octaves this thread's reference lies above `to`
+__device__ __forceinline__ float above(const Sums& t, float to, float c, float c4) {
+    return t.ordinary ? fmaf(-to, c, t.R) : octaves(t.ref, to, c4);
+}
+
 // move to another reference
-__device__ __forceinline__ void move_ref(Sums& t, float to, float c, bool plain) {
+__device__ __forceinline__ void move_ref(Sums& t, float to, float c, float c4, bool plain) {
     const Sums old = t;
     set_ref(t, to, c, plain);
     if (old.s == 0.f) t.a = 0.f;
-    else if (old.ordinary != t.ordinary) t.s = t.a = 0.f;
-    else shift(t, t.ordinary ? old.R - t.R : (old.ref - to) * c);
+    else shift(t, above(old, to, c, c4) + (t.ordinary ? fmaf(to, c, -t.R) : 0.f));  // (R's rounding)
 }
 
-__device__ __forceinline__ void add_one(Sums& t, float x, float c) {
+__device__ __forceinline__ void add_one(Sums& t, float x, float c, float c4) {
     // (an ordinary R is finite, any other ref is finite or +inf: -inf has no weight)
-    const float arg = exponent(t.ordinary ? fmaf(x, c, -t.R) : (x - t.ref) * c), e = ex2(arg);
+    const float arg = exponent(t.ordinary ? fmaf(x, c, -t.R) : octaves(x, t.ref, c4)), e = ex2(arg);
     t.s += e;
     t.a = fmaf(e, arg, t.a);
 }
@@ -210,8 +221,8 @@ __device__ __forceinline__ void append(const Search& q, float x, uint32_t id) {
 
 struct Args {
     int64_t V;
-    float c, inv_t;            // log2 e / T, 1 / T
-    bool plain;                // values of -1e30 have no weight beside ordinary ones
+    float c, c4, inv_t4;       // log2 e / T, and four times that; 4 / T
+    bool plain;                // c allows ordinary references
     const int32_t* tokens;
     int top_n;
     float *logprob, *entropy, *stats;
@@ -353,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
     }
     __syncthreads();
 
-    const float c = p.c;
+    const float c = p.c, c4 = p.c4;
     Sums t;
     set_ref(t, s_ref, c, p.plain);
     t.max = ninf;
@@ -364,15 +375,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
 
     if (edge >= 0) {
         const float x = edge_x;
-        if (!((x - t.ref) * c <= 64.f)) move_ref(t, fmaxf(x, t.ref), c, p.plain);
+        if (!((x - t.ref) * c <= 64.f)) move_ref(t, fmaxf(x, t.ref), c, c4, p.plain);
         t.max = fmaxf(t.max, x);
-        add_one(t, x, c);
+        add_one(t, x, c, c4);
         if (x >= bound && x > ninf) append(q, x, (uint32_t)edge);
     }
     auto take = [&](const uint4(&v)[kUnroll], int it) {
         const float cm = pieces_max<T>(v);
         t.max = fmaxf(t.max, cm);
-        if ((cm - t.ref) * c > 64.f) move_ref(t, cm, c, p.plain);
+        if ((cm - t.ref) * c > 64.f) move_ref(t, cm, c, c4, p.plain);
         // lanes that hold a candidate lay their pieces down, and the warp looks at them together,
         // one element a lane
         unsigned hits = __ballot_sync(kFullMask, cm >= bound);
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
                 float f[VE];
                 unpack<T>(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3], f);
 #pragma unroll
-                for (int e = 0; e < VE; ++e) add_one(t, f[e], c);
+                for (int e = 0; e < VE; ++e) add_one(t, f[e], c, c4);
             }
         }
     };
@@ -434,9 +445,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
 
     // ---- this run's sums, relative to its maximum ----
     auto combine = [&](float mx) {  // the block's sums at reference mx, valid in warp 0
-        const bool ordinary = p.plain && fabsf(mx) < 1e30f;
-        if (t.s == 0.f || t.ordinary != ordinary) t.s = t.s == t.s ? 0.f : t.s, t.a = 0.f;
-        else shift(t, ordinary ? fmaf(-mx, c, t.R) : (t.ref - mx) * c);
+        if (t.s == 0.f) t.a = 0.f;
+        else shift(t, above(t, mx, c, c4));
         const float s = warp_sum(t.s), a = warp_sum(t.a);
         if (lane == 0) part[warp][1] = s, part[warp][2] = a;
     };
@@ -537,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
                     r.a = ld_peer_f32(&run[3], lane);
                 }
                 const float all = warp_max(r.max);
-                if (r.s != 0.f) shift(r, (r.max - all) * c);
+                if (r.s != 0.f) shift(r, octaves(r.max, all, c4));
                 const float s = warp_sum(r.s), a = warp_sum(r.a);
                 __syncwarp();
                 if (lane == 0) part[0][0] = all, part[0][1] = s, part[0][2] = a;
@@ -561,10 +571,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
     const float top = part[0][0], s = part[0][1], a = part[0][2];
     const bool empty = top == ninf && s == 0.f;  // nothing can be produced
     const float logs = empty ? 0.f : logf(s);
+    auto nats = [&](float x) { return octaves(x, top, p.inv_t4); };  // (x - max) / T
     if (tid == 0) {
         if (p.logprob) {
             const float x = load_one(row + tok);
-            p.logprob[n] = empty ? ninf : (x - top) * p.inv_t - logs;
+            p.logprob[n] = empty ? ninf : nats(x) - logs;
         }
         if (p.entropy) p.entropy[n] = empty ? 0.f : fmaf(-kLn2, a / s, logs);
         if (p.stats) {
@@ -575,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
     if (tid < k) {
         const unsigned long long b = best[tid];
         p.top_ids[n * k + tid] = b ? (int32_t)candidate_id(b) : -1;
-        p.top_lp[n * k + tid] = b ? (key_float(candidate_key(b)) - top) * p.inv_t - logs : ninf;
+        p.top_lp[n * k + tid] = b ? nats(key_float(candidate_key(b))) - logs : ninf;
     }
 }
 
@@ -587,7 +598,7 @@ constexpr int kGradThreads = 256, kGradPieces = 4;
 
 struct GradArgs {
     int64_t V;
-    float c, inv_t;
+    float c4, temperature;  // 4 log2 e / T, T
     const int32_t* tokens;
     const float *stats, *entropy, *g_lp, *g_ent;
     int chunks;  // CTAs per row
@@ -605,14 +616,15 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const T* lo
     const int32_t tok = p.tokens ? p.tokens[n] : 0;
     const float max = p.stats[2 * n], logs = p.stats[2 * n + 1];
     const bool zero = tok < 0 || tok >= p.V || max == -INFINITY;
-    const float gl = !zero && p.g_lp ? p.g_lp[n] * p.inv_t : 0.f;
-    const float ge = !zero && p.g_ent ? p.g_ent[n] * p.inv_t : 0.f;
+    const float gl = !zero && p.g_lp ? p.g_lp[n] / p.temperature : 0.f;
+    const float ge = !zero && p.g_ent ? p.g_ent[n] / p.temperature : 0.f;
     const float h = !zero && p.g_ent ? p.entropy[n] : 0.f;
     // d = -p (gl + ge (log p + h)) = p (base + slope arg), arg = log2 p
-    const float l2 = logs * kLog2e, base = -fmaf(ge, h, gl), slope = -ge * kLn2;
+    const float l2 = logs * kLog2e, max4 = -0.25f * max, base = -fmaf(ge, h, gl), slope = -ge * kLn2;
     auto one = [&](float x, int64_t id) {
-        const float arg = exponent(fmaf(x - max, p.c, -l2));
-        float d = ex2(arg) * fmaf(slope, arg, base);
+        const float arg = exponent(fmaf(fmaf(x, 0.25f, max4), p.c4, -l2)), e = ex2(arg);
+        // (the weight first: slope times a far octave may pass float32, and the weight is 0 there)
+        float d = fmaf(e * arg, slope, e * base);
         if (id == tok) d += gl;
         return zero ? 0.f : d;
     };
@@ -727,8 +739,10 @@ extern "C" uno_status uno_token_logprobs(const void* logits, uno_dtype dtype, in
     const void* ptrs[] = {logits, tokens, out_logprob, out_entropy, out_stats, out_top_ids, out_top_logprobs};
     for (const void* p : ptrs)
         if (off16(p)) return set_error(UNO_ERR_UNSUPPORTED, "tensor pointers must be 16-byte aligned");
-    const Args a{V, (float)(1.4426950408889634 / (double)temperature), 1.0f / temperature, temperature < 1e20f, tokens,
-                 top_n, out_logprob, out_entropy, out_stats, out_top_ids, out_top_logprobs};
+    const float c = (float)(1.4426950408889634 / (double)temperature);
+    const Args a{V, c, (float)(4 * 1.4426950408889634 / (double)temperature), 4.0f / temperature,
+                 c > kMinC && c < kMaxC, tokens, top_n, out_logprob, out_entropy, out_stats, out_top_ids,
+                 out_top_logprobs};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return dtype == UNO_F32 ? logprobs_launch<float>(logits, N, a, st) : logprobs_launch<__nv_bfloat16>(logits, N, a, st);
 }
@@ -750,7 +764,7 @@ extern "C" uno_status uno_token_logprobs_grad(const void* logits, uno_dtype dtyp
     const void* ptrs[] = {logits, tokens, stats, entropy, grad_logprob, grad_entropy, grad_logits};
     for (const void* p : ptrs)
         if (off16(p)) return set_error(UNO_ERR_UNSUPPORTED, "tensor pointers must be 16-byte aligned");
-    const GradArgs a{V, (float)(1.4426950408889634 / (double)temperature), 1.0f / temperature, tokens, stats,
+    const GradArgs a{V, (float)(4 * 1.4426950408889634 / (double)temperature), temperature, tokens, stats,
                      entropy, grad_logprob, grad_entropy, 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return dtype == UNO_F32 ? grad_launch<float>(logits, grad_logits, N, a, st)

@@ -122,6 +122,7 @@ uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_scale, cons
  *
  * A row of nothing but -inf has log probability -inf, entropy 0, stats (-inf, 0) and no
  * alternatives. NaN and +inf logits make their row's numbers unspecified (NaN as a rule).
+ * Finite logits may be of any size; a log probability beyond float32 is -inf.
  * Limits: 1 <= V < 2^31 - 4096, N * V < 2^40, N < 2^31; temperature finite and at least
  * 1e-30. No workspace.
  * ====================================================================================== */
@@ -134,7 +135,8 @@ uno_status uno_token_logprobs(const void* logits, uno_dtype dtype, int64_t N, in
  *
  *   grad_logits[n, v] = ( grad_logprob[n] (1[v = tokens[n]] - p_v)
  *                         - grad_entropy[n] p_v (l[n, v] + entropy[n]) ) / temperature
- *   with p = exp(l); 0 on rows that are left out and on rows of nothing but -inf.
+ *   with p = exp(l); 0 on rows that are left out and on rows of nothing but -inf. A p below
+ *   2^-126 counts as 0.
  *
  *   logits, tokens, temperature: as given to uno_token_logprobs
  *   stats        [N, 2], entropy [N]: its out_stats and out_entropy

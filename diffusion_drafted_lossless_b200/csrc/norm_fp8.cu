@@ -459,7 +459,9 @@ uno_status norm_launch(const void* x, const void* residual, const void* weight, 
     const int most = M >= 4 * (int64_t)device_sms() ? 128 : kNormThreads;
     if (threads > most) threads = most;
     const size_t smem = (size_t)nvec * sizeof(Piece<T>);
-    if (smem > 48 * 1024) {  // (an attribute of the current device's function: set at each call)
+    // a launch has 48 KB without asking, its static part (`part`, and alignment) included. (An attribute
+    // of the current device's function: set at each call.)
+    if (smem > 47 * 1024) {
         const uno_status s = check_cuda(
             cudaFuncSetAttribute(norm_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 * (int)sizeof(T)),
             "cudaFuncSetAttribute(rms norm)");

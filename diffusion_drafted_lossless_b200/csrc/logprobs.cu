@@ -570,14 +570,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* __restri
     __syncthreads();
     const float top = part[0][0], s = part[0][1], a = part[0][2];
     const bool empty = top == ninf && s == 0.f;  // nothing can be produced
-    const float logs = empty ? 0.f : logf(s);
+    // (s has the maximum's own weight in it, 1: what falls below it are roundings, and no log
+    // probability is above 0, no entropy below; a NaN stays)
+    const float sure = s < 1.f ? 1.f : s, logs = empty ? 0.f : logf(sure);
     auto nats = [&](float x) { return octaves(x, top, p.inv_t4); };  // (x - max) / T
     if (tid == 0) {
         if (p.logprob) {
             const float x = load_one(row + tok);
             p.logprob[n] = empty ? ninf : nats(x) - logs;
         }
-        if (p.entropy) p.entropy[n] = empty ? 0.f : fmaf(-kLn2, a / s, logs);
+        if (p.entropy) {
+            const float h = empty ? 0.f : fmaf(-kLn2, a / sure, logs);
+            p.entropy[n] = h < 0.f ? 0.f : h;
+        }
         if (p.stats) {
             p.stats[2 * n] = top;
             p.stats[2 * n + 1] = logs;

@@ -122,7 +122,8 @@ uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_scale, cons
  *
  * A row of nothing but -inf has log probability -inf, entropy 0, stats (-inf, 0) and no
  * alternatives. NaN and +inf logits make their row's numbers unspecified (NaN as a rule).
- * Finite logits may be of any size; a log probability beyond float32 is -inf.
+ * Finite logits may be of any size; a log probability beyond float32 is -inf. No log
+ * probability is above 0 and no entropy below.
  * Limits: 1 <= V < 2^31 - 4096, N * V < 2^40, N < 2^31; temperature finite and at least
  * 1e-30. No workspace.
  * ====================================================================================== */

@@ -128,3 +128,20 @@ def test_entropy_gradient_where_a_weight_vanishes_beside_a_large_factor():
     ge = torch.tensor([1e6])
     g = _grad(x, None, None, ge, T)
     assert (g[0, 2:] == 0).all() and torch.isfinite(g).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_log_probabilities_and_entropies_keep_their_signs(dtype):
+    """One late token far above the sample holds all the weight: its probability is not above 1,
+    its alternatives' neither, and no entropy is negative."""
+    N, V = 300, 40000
+    g = torch.Generator().manual_seed(3)
+    x = torch.full((N, V), -1.0)
+    x[torch.arange(N), V - 3] = 20 + 20 * torch.rand(N, generator=g)
+    x = x.to(dtype)
+    tok = torch.full((N,), V - 3, dtype=torch.int32)
+    for T in (0.7, 1.0, 1e-9):
+        o = _run(x, tok, 2, T)
+        assert (o["logprob"] <= 0).all() and (o["lps"] <= 0).all() and (o["stats"][:, 1] >= 0).all()
+        assert (o["entropy"] >= 0).all()
+        _check(x, tok, o, 2, float(torch.tensor(T)))

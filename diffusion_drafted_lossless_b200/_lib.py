@@ -8,6 +8,7 @@ fallback path, and a missing or unloadable libuno.so is an error.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -126,6 +127,14 @@ def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return UNO_F32
     raise TypeError(f"unsupported dtype {t.dtype} (bf16 or fp32)")
+
+
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _allocating_on(stream):
+    """Allocations inside come from `stream`'s pool (None: the current stream's, as they do anyway)."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
 def _workspace(nbytes: int, device, workspace):
@@ -340,9 +349,10 @@ def uno_fp8_gated_lora_linear(x_q, x_scale, w_q, w_scale, y, x=None, lora_a=None
     if rank:
         nb = uno_fp8_gated_lora_linear_workspace_size(M, d_in, d_out, rank)
         if workspace is None:
-            workspace = lora_a.new_empty(nb >> 1)  # (bf16; nb is a multiple of 256 bytes)
-            if stream is not None and nb:
-                workspace.record_stream(stream)  # not handed out again before this stream is done with it
+            # from the pool of the stream that the call runs on: a block of another stream's may still be
+            # in use by what that one has queued (bf16; nb is a multiple of 256 bytes)
+            with _allocating_on(stream):
+                workspace = lora_a.new_empty(nb >> 1)
         elif workspace.get_device() != i:
             raise ValueError(f"workspace is on {workspace.device}, the tensors are on cuda:{i}")
         else:

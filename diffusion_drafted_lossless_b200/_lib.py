@@ -137,11 +137,12 @@ def _allocating_on(stream):
     return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
-def _workspace(nbytes: int, device, workspace):
+def _workspace(nbytes: int, device, workspace, stream):
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with _allocating_on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -165,7 +166,7 @@ def uno_gated_lora_linear(x, w0, lora_a, lora_b, row_gate, scale, y, workspace=N
     M, d_in = x.shape
     d_out, rank = w0.shape[0], lora_a.shape[0]
     code = _dtype_code(x)
-    ws, nb = _workspace(uno_gated_lora_linear_workspace_size(M, d_in, d_out, rank, code), x.device, workspace)
+    ws, nb = _workspace(uno_gated_lora_linear_workspace_size(M, d_in, d_out, rank, code), x.device, workspace, stream)
     _check(load().uno_gated_lora_linear(_ptr(x), _ptr(w0), _ptr(lora_a), _ptr(lora_b), _ptr(row_gate),
                                         float(scale), M, d_in, d_out, rank, code, _ptr(y), _ptr(ws), nb,
                                         _stream(stream)))
@@ -188,7 +189,7 @@ def uno_block_verify(verifier_logits, drafter_logits, temperature, top_k, top_p,
     B, K, V = verifier_logits.shape
     code = _dtype_code(verifier_logits)
     ws, nb = _workspace(uno_block_verify_workspace_size(B, K, V, top_k, top_p, code),
-                        verifier_logits.device, workspace)
+                        verifier_logits.device, workspace, stream)
     _check(load().uno_block_verify(
         _ptr(verifier_logits), _ptr(drafter_logits), code, B, K, V, float(temperature), int(top_k), float(top_p),
         _ptr(draft_tokens), _ptr(pos0_tokens), _ptr(uniforms), _ptr(out_tokens), _ptr(out_count),
@@ -218,7 +219,7 @@ def uno_tv_loss(teacher_logits, student_logits, out_tv, out_mean, grad_student=N
     """TV self-distillation loss and gradient over [N, V] logits (see include/uno.h)."""
     N, V = teacher_logits.shape
     code = _dtype_code(teacher_logits)
-    ws, nb = _workspace(uno_tv_loss_workspace_size(N, V, code), teacher_logits.device, workspace)
+    ws, nb = _workspace(uno_tv_loss_workspace_size(N, V, code), teacher_logits.device, workspace, stream)
     _check(load().uno_tv_loss(_ptr(teacher_logits), _ptr(student_logits), code, N, V, _ptr(response_mask),
                               float(grad_scale), _ptr(out_tv), _ptr(out_mean), _ptr(grad_student), _ptr(ws), nb,
                               _stream(stream)))

@@ -55,6 +55,23 @@ def test_fp8_linear_workspace_is_the_streams_own(monkeypatch, stream):
     assert pools.asked == ["side" if stream else "current"] and ran == [stream] and pools.active == "current"
 
 
+@pytest.mark.parametrize("stream", [None, "side"])
+@pytest.mark.parametrize("op", ["uno_gated_lora_linear", "uno_block_verify", "uno_tv_loss"])
+def test_other_workspaces_are_the_streams_own(monkeypatch, op, stream):
+    pools = _Pools(monkeypatch)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: pools.allocate(n))
+    monkeypatch.setattr(_lib, "load", lambda: types.SimpleNamespace(**{op: lambda *a: 0}))
+    monkeypatch.setattr(_lib, op + "_workspace_size", lambda *a: 512)
+    monkeypatch.setattr(_lib, "_ptr", lambda x: None)
+    monkeypatch.setattr(_lib, "_stream", lambda s: s)
+    t = lambda *s: types.SimpleNamespace(shape=torch.Size(s), dtype=BF, device="cuda:0")  # noqa: E731
+    args = {"uno_gated_lora_linear": (t(16, 64), t(64, 64), t(8, 64), t(64, 8), None, 1.0, t(16, 64)),
+            "uno_block_verify": (t(2, 4, 100), t(2, 4, 100), 1.0, 5, 0.9, t(2, 4, 3), t(2, 4), t(2)),
+            "uno_tv_loss": (t(4, 100), t(4, 100), t(4), t(1))}[op]
+    getattr(_lib, op)(*args, stream=stream)
+    assert pools.asked == ["side" if stream else "current"] and pools.active == "current"
+
+
 def _operands(M, d_in, d_out, rank):
     g = torch.Generator().manual_seed(M + d_out)
     o = {"xq": (60 * torch.randn((M, d_in), generator=g)).clamp(-448, 448).to(R.F8),

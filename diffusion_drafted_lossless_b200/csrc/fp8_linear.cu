@@ -421,6 +421,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
             const int m0 = (tile % p.m_tiles) * BM, n0 = (tile / p.m_tiles) * BN;
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = ok && (got < ST || wait_phase(&empty[s], ph, gave_up));
+                __syncwarp();  // (what is issued may end the next phase: a lane still polling would miss its own)
                 const bool low = kb >= p.nk8;
                 if (low && !waited) {
                     asm volatile("griddepcontrol.wait;\n\tfence.proxy.async.global;" ::: "memory");
@@ -437,7 +438,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                         load_2d(b, &tW, kb * 128, n0, &full[s]);
                     }
                 }
-                __syncwarp();  // (a lane left behind by two phases would wait for a third)
+                __syncwarp();
                 got += ok;
                 if (++s == ST) {
                     s = 0;
@@ -469,6 +470,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
             // (the two first polls are in flight together)
             const bool free = i < (uint32_t)NB || mbar_try_wait(&tempty[b], bph);
             ok = ok && wait_phase(&full[s], ph, gave_up) && (free || wait_longer(&tempty[b], bph, gave_up));
+            __syncwarp();  // (what is issued may end the next phases: a lane still polling would miss its own)
             fence_after();
             if (one && ok) {
                 const uint64_t da = da0 + (uint64_t)((s * a_bytes) >> 4), db = db0 + (uint64_t)((s * b_bytes) >> 4);
@@ -484,7 +486,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tX, const __grid_constant__ CU
                 commit(&tfull[b]);
                 commit(&empty[s]);
             }
-            __syncwarp();  // (a lane left behind by two phases would wait for a third)
+            __syncwarp();
             s += 2;
             if (s >= ST) {
                 s -= ST;

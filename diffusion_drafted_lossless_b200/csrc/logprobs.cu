@@ -46,10 +46,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// an exponent no lower than that of nothing; a NaN stays one
+// an exponent no lower than `least`, one of nothing; a NaN stays one
+template <int least = -2000>
 __device__ __forceinline__ float exponent(float x) {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-2000.f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"((float)least));
     return y;
 }
 
@@ -603,7 +604,7 @@ constexpr int kGradThreads = 256, kGradPieces = 4;
 
 struct GradArgs {
     int64_t V;
-    float c4, temperature;  // 4 log2 e / T, T
+    float c4, inv_t4;  // 4 log2 e / T, 4 / T
     const int32_t* tokens;
     const float *stats, *entropy, *g_lp, *g_ent;
     int chunks;  // CTAs per row
@@ -621,15 +622,15 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const T* lo
     const int32_t tok = p.tokens ? p.tokens[n] : 0;
     const float max = p.stats[2 * n], logs = p.stats[2 * n + 1];
     const bool zero = tok < 0 || tok >= p.V || max == -INFINITY;
-    const float gl = !zero && p.g_lp ? p.g_lp[n] / p.temperature : 0.f;
-    const float ge = !zero && p.g_ent ? p.g_ent[n] / p.temperature : 0.f;
+    const float gl = !zero && p.g_lp ? 0.25f * p.g_lp[n] * p.inv_t4 : 0.f;
+    const float ge = !zero && p.g_ent ? 0.25f * p.g_ent[n] * p.inv_t4 : 0.f;
     const float h = !zero && p.g_ent ? p.entropy[n] : 0.f;
     // d = -p (gl + ge (log p + h)) = p (base + slope arg), arg = log2 p
     const float l2 = logs * kLog2e, max4 = -0.25f * max, base = -fmaf(ge, h, gl), slope = -ge * kLn2;
     auto one = [&](float x, int64_t id) {
-        const float arg = exponent(fmaf(fmaf(x, 0.25f, max4), p.c4, -l2)), e = ex2(arg);
-        // (the weight first: slope times a far octave may pass float32, and the weight is 0 there)
-        float d = fmaf(e * arg, slope, e * base);
+        // (from -150 on the weight is 0, whatever its factor is: that stays inside float32)
+        const float arg = exponent<-150>(fmaf(fmaf(x, 0.25f, max4), p.c4, -l2));
+        float d = ex2(arg) * fmaf(slope, arg, base);
         if (id == tok) d += gl;
         return zero ? 0.f : d;
     };
@@ -769,7 +770,7 @@ extern "C" uno_status uno_token_logprobs_grad(const void* logits, uno_dtype dtyp
     const void* ptrs[] = {logits, tokens, stats, entropy, grad_logprob, grad_entropy, grad_logits};
     for (const void* p : ptrs)
         if (off16(p)) return set_error(UNO_ERR_UNSUPPORTED, "tensor pointers must be 16-byte aligned");
-    const GradArgs a{V, (float)(4 * 1.4426950408889634 / (double)temperature), temperature, tokens, stats,
+    const GradArgs a{V, (float)(4 * 1.4426950408889634 / (double)temperature), 4.0f / temperature, tokens, stats,
                      entropy, grad_logprob, grad_entropy, 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return dtype == UNO_F32 ? grad_launch<float>(logits, grad_logits, N, a, st)

@@ -144,7 +144,8 @@ uno_status uno_token_logprobs(const void* logits, uno_dtype dtype, int64_t N, in
  *   grad_logprob [N] float32 or NULL (zeros); needs tokens
  *   grad_entropy [N] float32 or NULL (zeros); needs entropy. At least one of the two.
  *   grad_logits  [N, V] dtype; may be logits itself
- * Limits as for uno_token_logprobs. No workspace.
+ * Limits as for uno_token_logprobs; |grad_entropy| / temperature up to 1e36 (beyond it a token's
+ * gradient may be NaN). No workspace.
  * ====================================================================================== */
 uno_status uno_token_logprobs_grad(const void* logits, uno_dtype dtype, int64_t N, int64_t V, float temperature,
                                    const int32_t* tokens, const float* stats, const float* entropy,

@@ -45,9 +45,11 @@ extern "C" {
  *   out_q       [M, d] e4m3, out_scale [M, ceil(d/128)] float32; both or neither
  *   out_y       [M, d] dtype or NULL: y rounded to dtype (what an adapter reads)
  *
- * Sums of squares in float32; a row whose sum passes its range comes out as NaN. Limits (else UNO_ERR_UNSUPPORTED): d a multiple of 16, d <=
- * 32768, M < 2^31. eps positive and finite; out_q or out_y has to be given; out_residual
- * needs residual. No workspace.
+ * Sums of squares in float32; a row whose sum passes its range comes out as NaN. bf16 rows hold
+ * the products h * weight in float32: one below 2^-126 in size keeps fewer bits, one above its
+ * range is infinite (float32 rows hold them in float64).
+ * Limits (else UNO_ERR_UNSUPPORTED): d a multiple of 16, d <= 32768, M < 2^31. eps positive and
+ * finite; out_q or out_y has to be given; out_residual needs residual. No workspace.
  * ====================================================================================== */
 uno_status uno_rms_norm_fp8(const void* x, const void* residual, const void* weight, uno_dtype dtype, int64_t M,
                             int64_t d, float eps, void* out_residual, void* out_q, float* out_scale, void* out_y,
@@ -82,7 +84,9 @@ uno_status uno_fp8_quantize(const void* x, uno_dtype dtype, int64_t rows, int64_
  *   y       [M, d_out] y_dtype (bf16; or f32 without an adapter)
  *
  * Arithmetic: each block of 128 columns is one tensor-core product of e4m3 values with
- * float32 accumulation, multiplied by its two scales and summed in float32. The adapter's
+ * float32 accumulation, multiplied by its two scales and summed in float32. (The product of the
+ * two scales is a float32 too: below 2^-126 it keeps fewer bits, above the range it is
+ * infinite.) The adapter's
  * X A^T is accumulated in float32 and rounded once to bf16; its product with B is
  * accumulated in float32 and multiplied by scale * g. A row whose scale * g is 0 gets no
  * adapter term. Y is rounded once to y_dtype. Sums are taken in an order fixed by the sizes.

@@ -160,19 +160,6 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void block_sync() { asm volatile("barrier.sync.aligned 0;" ::: "memory"); }
 __device__ __forceinline__ float4 ld_cluster(uint32_t local, uint32_t rank) {
     uint32_t remote;
@@ -197,19 +184,6 @@ __device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, vola
 }
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
     return mbar_try_wait(bar, parity) || wait_longer(bar, parity, gave_up);
-}
-
-// two columns of a row's float32 sums in a register pair
-__device__ __forceinline__ float2 columns(uint64_t v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-
-__device__ __forceinline__ uint64_t pair_of(float x, float y) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-    return v;
 }
 
 // acc[at / 2 ..] += f * r
@@ -253,8 +227,8 @@ __device__ __forceinline__ void store_rows(const Params& p, int row0, int col, i
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (k < K) {
-                const float2 a = columns(acc[4 * k % (CW / 2)]), b = columns(acc[(4 * k + 1) % (CW / 2)]),
-                             c = columns(acc[(4 * k + 2) % (CW / 2)]), d = columns(acc[(4 * k + 3) % (CW / 2)]);
+                const float2 a = two(acc[4 * k % (CW / 2)]), b = two(acc[(4 * k + 1) % (CW / 2)]),
+                             c = two(acc[(4 * k + 2) % (CW / 2)]), d = two(acc[(4 * k + 3) % (CW / 2)]);
                 v[k] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y), pack_bf16(c.x, c.y), pack_bf16(d.x, d.y));
             } else {
                 v[k] = make_uint4(0, 0, 0, 0);
@@ -276,7 +250,7 @@ __device__ __forceinline__ void store_rows(const Params& p, int row0, int col, i
         __nv_bfloat16* yb = static_cast<__nv_bfloat16*>(p.y) + o;
 #pragma unroll
         for (int j = 0; j < CW; j += 4) {
-            const float2 a = columns(acc[j / 2]), b = columns(acc[j / 2 + 1]);
+            const float2 a = two(acc[j / 2]), b = two(acc[j / 2 + 1]);
             if (p.y_f32 && p.N % 4 == 0) {
                 if (j < n) *reinterpret_cast<float4*>(yf + j) = make_float4(a.x, a.y, b.x, b.y);
             } else if (p.y_f32) {

@@ -7,14 +7,21 @@
 // (T, B). Each is one tensor-core product into a fresh TMEM accumulator, and the epilogue
 // warps add it, times its factor, into float32 registers:
 //   e4m3 block b:  acc += xs[m, b] ws[n / 128, b] * D        adapter:  acc += scale g[m] * D
-// so scales of any size cost one multiply-add per element and block, and the gate costs
-// nothing. T is made by the same kernel first: a product with adapter blocks alone (X, A) and
+// so the scales cost one multiply-add per element and block, whatever they are (xs ws is a float32
+// product, rounded once; below 2^-126 it keeps fewer bits), and the gate costs nothing.
+// T is rounded to bf16 because its product with B takes operands of one type (uno_gated_lora_linear
+// rounds its own too). Against 64 bits that is a small part of what Y's rounding is: all differences
+// of Y come to 1.8e-3 of its size with it and 1.7e-3 without (M 16 and M 1024). T in two bf16 parts
+// would double the adapter's K blocks.
+// T is made by the same kernel first: a product with adapter blocks alone (X, A) and
 // factor 1; the projection is launched to start on the SMs that this leaves free, and waits for
 // its end before it reads T (M 16, 4096 -> 4096, rank 128: 13.5 us, 19.1 one after the other).
 //
-// Bound: tensor cores for large M (M 8192, 2560 -> 9728: 216 us, 1885 TFLOP/s), HBM for few rows
-// of a wide head (M 64, 4096 -> 151936: 115 us, 5.6 TB/s), and between them the draining chain of
-// a tile's K blocks (M 16, 4096 -> 4096 without an adapter: 11 us for 17 MB).
+// Bound: tensor cores and draining for large M (M 8192, 2560 -> 9728: 214 us, 1907 TFLOP/s), HBM
+// for few rows of a wide head (M 64, 4096 -> 151936: 113 us, 5.7 TB/s), and between them the draining
+// chain of a tile's K blocks (M 16, 4096 -> 4096 without an adapter: 9.5 us for 17 MB from HBM,
+// 8.3 from L2). These are at 1965 MHz, as a burst finds the SMs; the power limit lowers the clock
+// of a second of the same to 1575 MHz, and times follow it: 245 and 133 us.
 //
 // Roles of a CTA's warps: 0 loads K blocks by TMA into a ring of shared-memory stages; 1 and 2
 // issue tcgen05.mma for the even and the odd K blocks, each into accumulators of its own
@@ -220,7 +227,8 @@ __device__ __forceinline__ void exchange(uint4 (&v)[8], int lane) {
 
 // CW columns from `col` on of rows row0 + lane (this warp's 32 rows)
 template <int CW>
-__device__ __forceinline__ void store_rows(const Params& p, int row0, int col, int lane, const uint64_t (&acc)[CW / 2]) {
+__device__ __forceinline__ void store_rows(const Params& p, int row0, int col, int lane,
+                                           const uint64_t (&acc)[CW / 2]) {
     if (!p.y_f32 && p.N % 8 == 0) {  // rows of bf16 that start on 16 bytes: by whole lines
         constexpr int K = CW / 8;    // chunks of 8 columns: eight, or four
         uint4 v[8];
@@ -730,7 +738,8 @@ uno_status facts_of(int sms, Facts& f) {
         s = check_cuda(cudaFuncSetAttribute(linear_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem),
                        "cudaFuncSetAttribute(fp8 linear)");
         cudaFuncAttributes a;
-        if (s == UNO_OK) s = check_cuda(cudaFuncGetAttributes(&a, linear_kernel<F>), "cudaFuncGetAttributes(fp8 linear)");
+        if (s == UNO_OK)
+            s = check_cuda(cudaFuncGetAttributes(&a, linear_kernel<F>), "cudaFuncGetAttributes(fp8 linear)");
         if (s != UNO_OK) return s;
         // the kernel's register split waits for what the launch did not bring
         if (F::split && a.numRegs < F::regs)
@@ -749,7 +758,8 @@ uno_status facts_of(int sms, Facts& f) {
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
             int n = 0;
-            s = check_cuda(cudaOccupancyMaxActiveClusters(&n, linear_kernel<F>, &cfg), "cudaOccupancyMaxActiveClusters");
+            s = check_cuda(cudaOccupancyMaxActiveClusters(&n, linear_kernel<F>, &cfg),
+                           "cudaOccupancyMaxActiveClusters");
             if (s != UNO_OK) return s;
             k |= (uint64_t)(n < 0xFFFF ? n : 0xFFFF) << (16 * i);
         }
@@ -786,8 +796,8 @@ uno_status choose(int64_t M, int64_t N, int nk, int sms, int beside, Shape& c) {
         c = shape_of<Wide>(M, 1);
         return facts_of<Wide>(sms, f);
     }
-    // The form with fewer K blocks in turn; M 16, 4096 -> 4096: 8 with 128 columns and clusters of
-    // four, 8.3 us, 16 with 64 columns and clusters of two, 10.9. Where both have as many, the one
+    // The form with fewer K blocks in turn; M 16, 4096 -> 4096 from L2: 8 with 128 columns and clusters
+    // of four, 8.3 us, 16 with 64 columns and clusters of two, 10.9. Where both have as many, the one
     // whose block is shorter: M 37, 4992 -> 700: 64 columns 6.9 us, 128 columns 7.4.
     Shape c64;
     int64_t in_turn, in_turn64;
@@ -902,16 +912,18 @@ extern "C" uno_status uno_fp8_gated_lora_linear(const void* x_q, const float* x_
     if (M < 0 || d_in < 1 || d_out < 1 || rank < 0)
         return set_error(UNO_ERR_INVALID_ARG, "need M >= 0, d_in >= 1, d_out >= 1, rank >= 0");
     if (d_in % 16 || d_in > 65536 || d_out > (1 << 20) || M > (1 << 20))
-        return set_error(UNO_ERR_UNSUPPORTED, "d_in a multiple of 16 up to 65536, d_out and M up to 2^20 are supported");
+        return set_error(UNO_ERR_UNSUPPORTED,
+                         "d_in a multiple of 16 up to 65536, d_out and M up to 2^20 are supported");
     if (rank % 8 || rank > 256) return set_error(UNO_ERR_UNSUPPORTED, "rank must be 0 or a multiple of 8 and <= 256");
     if (rank && y_dtype == UNO_F32) return set_error(UNO_ERR_UNSUPPORTED, "float32 output is supported with rank 0");
     // tiles times K blocks: they are counted over a CTA's tiles in 32 bits
-    if ((M + 127) / 128 * (M > 64 ? (d_out + 255) / 256 : (d_out + 127) / 128) * ((d_in + 127) / 128 + (rank + 63) / 64) >
-        0x7FFFFFFF)
+    const int64_t tiles = (M + 127) / 128 * (M > 64 ? (d_out + 255) / 256 : (d_out + 127) / 128);
+    if (tiles * ((d_in + 127) / 128 + (rank + 63) / 64) > 0x7FFFFFFF)
         return set_error(UNO_ERR_UNSUPPORTED, "too many output tiles");
     if (M == 0) return UNO_OK;
     if (!x_q || !x_scale || !w_q || !w_scale || !y) return set_error(UNO_ERR_INVALID_ARG, "a tensor pointer is NULL");
-    if (rank && (!x || !lora_a || !lora_b)) return set_error(UNO_ERR_INVALID_ARG, "rank > 0 needs x, lora_a and lora_b");
+    if (rank && (!x || !lora_a || !lora_b))
+        return set_error(UNO_ERR_INVALID_ARG, "rank > 0 needs x, lora_a and lora_b");
     if (rank && !(std::isfinite(scale))) return set_error(UNO_ERR_INVALID_ARG, "scale must be finite");
     const void* ptrs[] = {x_q, x_scale, w_q, w_scale, y};
     for (const void* p : ptrs)

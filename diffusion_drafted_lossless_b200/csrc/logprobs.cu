@@ -20,9 +20,10 @@
 // what beats it, until the list holds everything. Each such reading leaves about top_n of 2048 of
 // what it finds, whatever the order (600 rows of 151936 bf16 that rise to their middle and fall:
 // 0.89 ms in place of 4.9 with a list of the first and latest ones; in no order: 0.065).
-// Measured: 2048 rows of 166144 bf16, 40% left out, 5 alternatives: 81-88 us, 4.6-5.0 TB/s; 16 rows
-// of 151936, 20 alternatives: 10.5 us (eight CTAs a row; ranking and joining take half). With its
-// gradient, 1024 rows of 151936: 161 us, the logits read twice and the gradient written once.
+// Measured: 2048 rows of 166144 bf16, 40% left out, 5 alternatives: 82 us, 5.0 TB/s; 16 rows of
+// 151936, 20 alternatives: 10.9 us (eight CTAs a row; ranking and joining take half). With its
+// gradient, 1024 rows of 151936: 157 us, 160 in a second-long run (1880 MHz), the logits read twice
+// and the gradient written once.
 #include <cmath>
 #include <type_traits>
 
@@ -736,7 +737,8 @@ extern "C" uno_status uno_token_logprobs(const void* logits, uno_dtype dtype, in
                  c > kMinC && c < kMaxC, tokens, top_n, out_logprob, out_entropy, out_stats, out_top_ids,
                  out_top_logprobs};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return dtype == UNO_F32 ? logprobs_launch<float>(logits, N, a, st) : logprobs_launch<__nv_bfloat16>(logits, N, a, st);
+    return dtype == UNO_F32 ? logprobs_launch<float>(logits, N, a, st)
+                            : logprobs_launch<__nv_bfloat16>(logits, N, a, st);
 }
 
 extern "C" uno_status uno_token_logprobs_grad(const void* logits, uno_dtype dtype, int64_t N, int64_t V,

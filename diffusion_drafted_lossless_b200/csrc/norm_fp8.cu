@@ -7,7 +7,8 @@
 // do. The quotient 448 u / a is what is rounded, once, to nearest even:
 // Found in float32 as u c + u r, with c near 448 / a and r its remainder, it is off by its last
 // rounding, 2^-24, and no more:
-//   bf16 inputs: u is exact in float32 (a product of two 8-bit significands). 448 u and
+//   bf16 inputs: u is exact in float32 (a product of two 8-bit significands), but for products below
+//     its normal numbers or beyond it, which the norm takes as float32 has them. 448 u and
 //     border * a are whole numbers of at most 21 bits on a common scale, so a quotient that is
 //     not on a border of e4m3 is at least 2^-21 away from it, and one that is on it comes out
 //     exactly: the values are those of exact arithmetic.
@@ -19,9 +20,10 @@
 // Bound: HBM. The norm reads x and the residual and writes h, the values and, if asked, y,
 // each once; a row is held in shared memory between its sum of squares and its values (16
 // bytes a thread at a time, read back by the thread that wrote them). One CTA per row.
-// Measured: the norm of 16384 x 2560 bf16 with a residual 51 us, 5.8 TB/s; 16 x 4096 2.3 us (one
-// row's latency); the quantiser on 1024 x 12288 float32 14.0 us, 4.5 TB/s, and on 9728 x 2560 bf16
-// by 128 x 128 blocks 14.2 us, 5.3 TB/s (sizes near that of L2, a launch's ramp in each).
+// Measured: the norm of 16384 x 2560 with a residual 51 us, 5.8 TB/s, in bf16 and 105 us, 5.2 TB/s,
+// in float32; of 16 x 4096 2.4 and 3.8 us (one row's latency); the quantiser on 1024 x 12288 float32
+// 14.4 us, 4.4 TB/s, and on 9728 x 2560 by 128 x 128 blocks 14.6 us, 5.1 TB/s, in bf16 and 24.4 us,
+// 5.1 TB/s, in float32 (sizes near that of L2, a launch's ramp in each).
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -399,15 +401,16 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
 
 // 128 x 128 blocks: a CTA holds one in registers, four or eight pieces a thread. Its loads, its
 // maximum and its stores come one after the other, so other CTAs have to fill the gaps: three of
-// 256 threads an SM take 14.2 us for 9728 x 2560 bf16, two of 512 16.8 (float32, whose pieces take
+// 256 threads an SM take 14.6 us for 9728 x 2560 bf16, two of 512 16.8 (float32, whose pieces take
 // twice the registers: two of 512 23.4, of 256 26.9).
 template <typename T>
 constexpr int kBlockThreads = std::is_same_v<T, float> ? 512 : 256;
 template <typename T>
 constexpr int kBlockCtas = std::is_same_v<T, float> ? 2 : 3;  // per SM, as registers allow
 template <typename T>
-__global__ void __launch_bounds__(kBlockThreads<T>, kBlockCtas<T>) quantize_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
-                                                              uint8_t* __restrict__ q, float* __restrict__ scale) {
+__global__ void __launch_bounds__(kBlockThreads<T>, kBlockCtas<T>)
+quantize_blocks_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, uint8_t* __restrict__ q,
+                       float* __restrict__ scale) {
     constexpr int NT = kBlockThreads<T>, N = 128 * kLanes / NT;
     __shared__ float part[NT / 32];
     const int64_t nblocks = (cols + kBlockCols - 1) / kBlockCols;
@@ -489,8 +492,8 @@ uno_status quantize_launch(const void* x, int64_t rows, int64_t cols, int block_
     } else {
         const int64_t blocks = ((rows + 127) / 128) * ((cols + kBlockCols - 1) / kBlockCols);
         if (blocks > 0x7FFFFFFF) return set_error(UNO_ERR_UNSUPPORTED, "more than 2^31 - 1 blocks");
-        quantize_blocks_kernel<T><<<(unsigned)blocks, kBlockThreads<T>, 0, stream>>>(static_cast<const T*>(x), rows, cols,
-                                                                       static_cast<uint8_t*>(q), scale);
+        quantize_blocks_kernel<T><<<(unsigned)blocks, kBlockThreads<T>, 0, stream>>>(
+            static_cast<const T*>(x), rows, cols, static_cast<uint8_t*>(q), scale);
     }
     return check_cuda(cudaGetLastError(), "launch(fp8 quantize)");
 }

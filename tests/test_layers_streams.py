@@ -133,3 +133,31 @@ def test_calls_on_two_streams_at_once_without_a_workspace():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(alone, outs))
     assert _lib.uno_read_device_status() == _lib.UNO_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rank", [0, 64])
+def test_launches_that_start_early_on_two_streams_at_once(rank):
+    """Calls of two and three launches, each started beside the one before it on its stream, on two streams
+    with nothing waited for between them: the bits that each has alone."""
+    shapes, streams = ((40, 4096, 19200), (642, 4096, 12584), (16, 4096, 4096)), (torch.cuda.Stream(), torch.cuda.Stream())
+    sets = []
+    for M, d_in, d_out in shapes:
+        c = _operands(M, d_in, d_out, max(rank, 8))
+        if not rank:
+            c["a"] = c["b"] = c["x"] = c["gate"] = None
+        ys = [torch.empty((M, d_out), dtype=BF, device="cuda") for _ in range(3)]
+        sets.append((c, _run(c, ys[0]), ys[1:]))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i in range(len(sets)):
+            for k, st in enumerate(streams):
+                c, _, ys = sets[(i + k) % len(sets)]
+                _run(c, ys[k], stream=st)
+        torch.cuda.synchronize()
+        for _, alone, ys in sets:
+            assert all(torch.equal(alone, y) for y in ys)
+            for y in ys:
+                y.zero_()
+        torch.cuda.synchronize()
+    assert _lib.uno_read_device_status() == _lib.UNO_OK

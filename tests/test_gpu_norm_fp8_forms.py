@@ -30,7 +30,8 @@ assert ((y - 1).abs() <= 1e-6).all()  # (1 / sqrt(1 + eps), half of eps below 1)
 @pytest.mark.parametrize("dtype,d", [("float32", 12272), ("float32", 12288), ("bfloat16", 24544), ("bfloat16", 24560),
                                      ("bfloat16", 24576)])
 def test_first_call_of_a_process(dtype, d):
-    r = subprocess.run([sys.executable, "-c", FIRST, dtype, str(d)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", FIRST, dtype, str(d)], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
 
 
@@ -47,8 +48,9 @@ def _check(x, w, r, inplace):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("M,d,res,inplace", [(592, 128, True, False), (600, 2576, True, True), (593, 4112, False, False),
-                                             (700, 4112, True, False), (640, 1040, True, True), (600, 16, False, False)])
+@pytest.mark.parametrize("M,d,res,inplace", [(592, 128, True, False), (600, 2576, True, True),
+                                             (593, 4112, False, False), (700, 4112, True, False),
+                                             (640, 1040, True, True), (600, 16, False, False)])
 def test_many_rows(M, d, res, inplace, dtype):
     """From four rows an SM on: several turns of a CTA's 128 threads, the last of them partial."""
     assert M >= 4 * torch.cuda.get_device_properties(0).multi_processor_count

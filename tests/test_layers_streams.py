@@ -140,7 +140,8 @@ def test_calls_on_two_streams_at_once_without_a_workspace():
 def test_launches_that_start_early_on_two_streams_at_once(rank):
     """Calls of two and three launches, each started beside the one before it on its stream, on two streams
     with nothing waited for between them: the bits that each has alone."""
-    shapes, streams = ((40, 4096, 19200), (642, 4096, 12584), (16, 4096, 4096)), (torch.cuda.Stream(), torch.cuda.Stream())
+    shapes = ((40, 4096, 19200), (642, 4096, 12584), (16, 4096, 4096))
+    streams = (torch.cuda.Stream(), torch.cuda.Stream())
     sets = []
     for M, d_in, d_out in shapes:
         c = _operands(M, d_in, d_out, max(rank, 8))
